@@ -94,6 +94,7 @@ def lib() -> ctypes.CDLL:
         L.saf3r_last_launch_count.restype = i32
         L.saf3r_status_string.argtypes = [i32]
         L.saf3r_status_string.restype = ctypes.c_char_p
+        streaming.declare(L)
         _lib = L
     return _lib
 
@@ -364,3 +365,7 @@ def header_functions() -> List[str]:
     txt = open(HEADER_PATH).read()
     txt = re.sub(r"/\*.*?\*/", "", txt, flags=re.S)
     return sorted(set(re.findall(r"\b(saf3r_[a-z_0-9]+)\s*\(", txt)))
+
+
+from . import streaming  # noqa: E402  (it uses the helpers above)
+from .streaming import *  # noqa: E402,F401,F403

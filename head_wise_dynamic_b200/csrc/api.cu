@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "stream.h"
 
 
 using namespace saf3r;
@@ -686,6 +687,40 @@ bool saf3r::make_map_f16_rows(CUtensorMap* m, const void* base, long long rows, 
   cuuint32_t box[2] = {64, 128};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ------------------------------------------------------------------ shared with stream_api.cu
+bool saf3r::call_device(int* sms, int* major, int** err) {
+  DeviceInfo d;
+  if (!device_info(d)) return false;
+  *sms = d.sms;
+  *major = d.major;
+  *err = d.err;
+  return true;
+}
+
+void saf3r::set_launch_count(int n) { t_launches = n; }
+
+long long saf3r::call_wait_budget() { return t_wait_budget; }
+
+bool saf3r::take_withhold_arrive() {
+  const bool w = t_withhold_arrive;
+  t_withhold_arrive = false;
+  return w;
+}
+
+// [heads][rows][64] bf16 rows with any strides (elements), box_rows x 64 boxes, 128-byte swizzle, zero fill.
+bool saf3r::make_map_rows(CUtensorMap* m, const void* base, long long rows, long long row_stride, int heads,
+                          long long head_stride, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride) * 2, static_cast<cuuint64_t>(head_stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

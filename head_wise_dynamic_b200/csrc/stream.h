@@ -1,0 +1,138 @@
+// Plans of the streaming operators (rotary positions, paged key/value append, attention over the
+// cache), shared by their kernels and the host side.  Not part of the C ABI.
+#pragma once
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace saf3r {
+
+// Rotation table of a head's 64 dims in 8 groups of 8 values: group g holds dims o1[g]..+3 and
+// o2[g]..+3.  Groups below n_groups turn four pairs each (pairs 4g..4g+3), the others are copied.
+// freq is the turn per position in units of 2^-64 turns, so pos * freq modulo 2^64 is the angle's
+// fraction of a turn with no reduction error at any int32 position.
+struct RopeTable {
+  uint64_t freq[32];
+  int8_t axis[8], o1[8], o2[8];
+  int32_t n_groups;
+  int32_t interleaved;  // pairs (0,1),(2,3) of each half of a group, and o2 = o1 + 4; else (o1 + i, o2 + i)
+  int32_t n_axes;
+};
+
+struct RopeParams {
+  RopeTable table;
+  const void* x;
+  void* out;
+  const int32_t* pos;
+  long long n_tokens, x_ts, x_hs, out_ts, out_hs;
+  int32_t n_heads, n_rot, inverse, heads_per_block;
+};
+
+// A batch's device arrays and the cache, as the kernels see them.
+struct KvView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* cu;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int* err;
+  int32_t n_pages, n_heads, page, page_log2;
+  int32_t n_seqs, n_tokens, max_new, max_pages;
+};
+
+struct AppendParams {
+  KvView kv;
+  RopeTable rope;
+  int32_t has_rope, heads_per_block;
+  const uint16_t* k_rows;
+  const uint16_t* v_rows;
+  long long k_ts, k_hs, v_ts, v_hs;
+  const int32_t* pos;
+};
+
+struct WindowMask {
+  int32_t view, window, sink, causal;
+};
+
+struct KvAttnParams {
+  KvView kv;
+  WindowMask win;
+  const uint16_t* q;
+  void* out;
+  long long q_ts, q_hs, out_ts, out_hs;
+  int32_t n_heads, group, out_fp32;
+  uint8_t* ws;
+  int32_t num_sms;
+  long long wait_budget;
+  int32_t withhold;
+};
+
+#ifdef __CUDACC__
+
+// Sequence b of a batch: its rows, cached length and whether the numbers fit.
+struct SeqInfo {
+  int row0, n_new, len;
+  bool ok;
+};
+__device__ __forceinline__ SeqInfo seq_info(const KvView& kv, int b) {
+  SeqInfo s;
+  s.row0 = kv.cu[b];
+  const int end = kv.cu[b + 1];
+  s.len = kv.kv_lens[b];
+  s.n_new = end - s.row0;
+  s.ok = s.row0 >= 0 && end >= s.row0 && end <= kv.n_tokens && s.n_new <= kv.max_new && s.len >= s.n_new &&
+         s.len <= (static_cast<long long>(kv.max_pages) << kv.page_log2);
+  if (!s.ok) {
+    atomicCAS(kv.err, 0, SAF3R_ERR_INDEX);
+    s.row0 = s.n_new = s.len = 0;
+  }
+  return s;
+}
+
+// The keys a query at position p of a sequence of len tokens sees: [lo, hi) and [0, sink).
+struct Span {
+  int lo, hi, sink;
+};
+__device__ __forceinline__ Span span_of(const WindowMask& w, int p, int len) {
+  const long long f = p / w.view;
+  Span s;
+  s.lo = 0;
+  if (w.window > 0 && f - w.window + 1 > 0) s.lo = static_cast<int>((f - w.window + 1) * w.view);
+  const long long end = w.causal ? (f + 1) * w.view : (w.window > 0 ? (f + w.window) * w.view : len);
+  s.hi = end < len ? static_cast<int>(end) : len;
+  s.sink = min(w.sink, w.causal ? s.hi : len);
+  return s;
+}
+
+__device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int pos, float& s, float& c) {
+  const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * t.freq[pair];
+  // upper 32 bits as a signed fraction of a turn, in half turns: [-1, 1)
+  const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
+  sincospif(x, &s, &c);
+}
+
+#endif
+
+bool build_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t);
+cudaError_t launch_rope(const RopeParams& p, bool in_fp32, bool out_fp32, cudaStream_t stream, int* n_launch);
+cudaError_t launch_append(const AppendParams& p, bool e4m3, int num_sms, cudaStream_t stream, int* n_launch);
+
+// few query rows per sequence and kv head (kv_decode.cu)
+bool decode_takes(int max_new, int group);
+size_t decode_workspace_bytes(const KvView& kv, const WindowMask& w, int n_heads, int num_sms);
+cudaError_t launch_decode(const KvAttnParams& p, bool e4m3, cudaStream_t stream, int* n_launch);
+
+// host side of api.cu that the streaming entry points share
+bool call_device(int* sms, int* major, int** err);
+void set_launch_count(int n);
+long long call_wait_budget();
+bool take_withhold_arrive();
+bool make_map_rows(CUtensorMap* m, const void* base, long long rows, long long row_stride, int heads,
+                   long long head_stride, int box_rows);
+
+}  // namespace saf3r

@@ -1,0 +1,169 @@
+// C ABI of the streaming operators: argument checks, views of the caller's buffers, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "stream.h"
+
+using namespace saf3r;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Row strides of a tensor that is read (broadcast dims allowed) or written (rows must not overlap).
+bool strides_ok(long long tokens, long long ts, long long heads, long long hs, bool fp32, bool written) {
+  const long long unit = fp32 ? 4 : 8, top = 1LL << 36;
+  if (ts < 0 || hs < 0 || ts % unit || hs % unit || ts > top || hs > top) return false;
+  if (!written) return true;
+  if ((tokens > 1 && ts < kD) || (heads > 1 && hs < kD)) return false;
+  if (tokens > 1 && heads > 1) {
+    // rows apart: one dim lies inside the other's step
+    const bool token_major = ts >= (heads - 1) * hs + kD, head_major = hs >= (tokens - 1) * ts + kD;
+    if (!token_major && !head_major) return false;
+  }
+  return true;
+}
+
+saf3r_status check_cache(const saf3r_kv_cache* c, bool pointers) {
+  if (!c) return SAF3R_ERR_INVALID;
+  if (c->n_pages < 1 || c->n_heads < 1 || c->n_heads > kMaxHeads) return SAF3R_ERR_INVALID;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return SAF3R_ERR_INVALID;
+  if (c->type != SAF3R_KV_BF16 && c->type != SAF3R_KV_E4M3) return SAF3R_ERR_INVALID;
+  // rows of a pool are counted in 31 bits
+  if (static_cast<long long>(c->n_pages) * c->n_heads * c->page >= (1LL << 31)) return SAF3R_ERR_UNSUPPORTED;
+  if (!pointers) return SAF3R_OK;
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return SAF3R_ERR_INVALID;
+  if (c->type == SAF3R_KV_E4M3 &&
+      (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
+    return SAF3R_ERR_INVALID;
+  return SAF3R_OK;
+}
+
+saf3r_status check_batch(const saf3r_kv_cache* c, const saf3r_kv_batch* b, bool pointers) {
+  if (!b || b->n_seqs < 0 || b->n_seqs > 65535 || b->n_tokens < 0 || b->max_new < 0 || b->max_new > b->n_tokens ||
+      b->max_pages < 0)
+    return SAF3R_ERR_INVALID;
+  // positions are counted in 31 bits, with room for one tile behind the last
+  if (static_cast<long long>(b->max_pages) * c->page > (1LL << 31) - 1024) return SAF3R_ERR_UNSUPPORTED;
+  if (pointers && b->n_seqs > 0 &&
+      (!b->cu_tokens || !b->kv_lens || (b->max_pages > 0 && !b->page_table) ||
+       (reinterpret_cast<uintptr_t>(b->cu_tokens) & 3) || (reinterpret_cast<uintptr_t>(b->kv_lens) & 3) ||
+       (reinterpret_cast<uintptr_t>(b->page_table) & 3)))
+    return SAF3R_ERR_INVALID;
+  return SAF3R_OK;
+}
+
+bool window_ok(const saf3r_window* w) { return w && w->view_tokens >= 1 && w->window >= 0 && w->n_sink >= 0; }
+
+KvView view_of(const saf3r_kv_cache* c, const saf3r_kv_batch* b, int* err) {
+  KvView v;
+  v.k = static_cast<uint8_t*>(c->k);
+  v.v = static_cast<uint8_t*>(c->v);
+  v.k_scale = c->k_scale;
+  v.v_scale = c->v_scale;
+  v.cu = b->cu_tokens;
+  v.kv_lens = b->kv_lens;
+  v.table = b->page_table;
+  v.err = err;
+  v.n_pages = c->n_pages;
+  v.n_heads = c->n_heads;
+  v.page = c->page;
+  v.page_log2 = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  v.n_seqs = b->n_seqs;
+  v.n_tokens = b->n_tokens;
+  v.max_new = b->max_new;
+  v.max_pages = b->max_pages;
+  return v;
+}
+
+WindowMask mask_of(const saf3r_window* w) { return WindowMask{w->view_tokens, w->window, w->n_sink, w->causal != 0}; }
+
+saf3r_status device(int* sms, int** err) {
+  int major = 0;
+  if (!call_device(sms, &major, err)) return SAF3R_ERR_CUDA;
+  return major == 10 ? SAF3R_OK : SAF3R_ERR_UNSUPPORTED;
+}
+
+saf3r_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SAF3R_OK : SAF3R_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+saf3r_status saf3r_rope(const saf3r_rope_cfg* rope, const saf3r_rope_args* a, void* stream) {
+  set_launch_count(0);
+  RopeParams p;
+  if (!build_rope_table(rope, &p.table) || !a) return SAF3R_ERR_INVALID;
+  if (a->n_tokens < 0 || a->n_tokens >= (1LL << 31) || a->n_heads < 0 || a->n_heads > 65535 || a->n_rot_heads < 0 ||
+      a->n_rot_heads > a->n_heads)
+    return SAF3R_ERR_INVALID;
+  if (a->n_tokens == 0 || a->n_heads == 0) return SAF3R_OK;
+  if (!a->x || !a->out || !aligned16(a->x) || !aligned16(a->out)) return SAF3R_ERR_INVALID;
+  if (a->n_rot_heads > 0 && (!a->pos || (reinterpret_cast<uintptr_t>(a->pos) & 3))) return SAF3R_ERR_INVALID;
+  if (!strides_ok(a->n_tokens, a->x_token_stride, a->n_heads, a->x_head_stride, a->x_is_fp32 != 0, false) ||
+      !strides_ok(a->n_tokens, a->out_token_stride, a->n_heads, a->out_head_stride, a->out_is_fp32 != 0, true))
+    return SAF3R_ERR_INVALID;
+  if (a->x == a->out && ((a->x_is_fp32 != 0) != (a->out_is_fp32 != 0) || a->x_token_stride != a->out_token_stride ||
+                         a->x_head_stride != a->out_head_stride))
+    return SAF3R_ERR_INVALID;
+  int sms = 0, *err = nullptr;
+  const saf3r_status st = device(&sms, &err);
+  if (st != SAF3R_OK) return st;
+  p.x = a->x;
+  p.out = a->out;
+  p.pos = a->pos;
+  p.n_tokens = a->n_tokens;
+  p.x_ts = a->x_token_stride;
+  p.x_hs = a->x_head_stride;
+  p.out_ts = a->out_token_stride;
+  p.out_hs = a->out_head_stride;
+  p.n_heads = a->n_heads;
+  p.n_rot = a->n_rot_heads;
+  p.inverse = a->inverse != 0;
+  p.heads_per_block = 0;
+  int launches = 0;
+  const cudaError_t e =
+      launch_rope(p, a->x_is_fp32 != 0, a->out_is_fp32 != 0, static_cast<cudaStream_t>(stream), &launches);
+  set_launch_count(launches);
+  return cuda_status(e);
+}
+
+saf3r_status saf3r_kv_append(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch, const saf3r_rope_cfg* rope,
+                             const saf3r_kv_rows* rows, void* stream) {
+  set_launch_count(0);
+  saf3r_status st = check_cache(cache, true);
+  if (st != SAF3R_OK) return st;
+  if ((st = check_batch(cache, batch, true)) != SAF3R_OK) return st;
+  AppendParams p;
+  std::memset(&p.rope, 0, sizeof(p.rope));
+  if (rope && !build_rope_table(rope, &p.rope)) return SAF3R_ERR_INVALID;
+  if (!rows) return SAF3R_ERR_INVALID;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0 || batch->max_new == 0) return SAF3R_OK;
+  if (!rows->k || !rows->v || !aligned16(rows->k) || !aligned16(rows->v)) return SAF3R_ERR_INVALID;
+  if (rope && (!rows->pos || (reinterpret_cast<uintptr_t>(rows->pos) & 3))) return SAF3R_ERR_INVALID;
+  if (!strides_ok(batch->n_tokens, rows->k_token_stride, cache->n_heads, rows->k_head_stride, false, false) ||
+      !strides_ok(batch->n_tokens, rows->v_token_stride, cache->n_heads, rows->v_head_stride, false, false))
+    return SAF3R_ERR_INVALID;
+  int sms = 0, *err = nullptr;
+  if ((st = device(&sms, &err)) != SAF3R_OK) return st;
+  p.kv = view_of(cache, batch, err);
+  p.has_rope = rope != nullptr;
+  p.heads_per_block = 0;
+  p.k_rows = static_cast<const uint16_t*>(rows->k);
+  p.v_rows = static_cast<const uint16_t*>(rows->v);
+  p.k_ts = rows->k_token_stride;
+  p.k_hs = rows->k_head_stride;
+  p.v_ts = rows->v_token_stride;
+  p.v_hs = rows->v_head_stride;
+  p.pos = rows->pos;
+  int launches = 0;
+  const cudaError_t e =
+      launch_append(p, cache->type == SAF3R_KV_E4M3, sms, static_cast<cudaStream_t>(stream), &launches);
+  set_launch_count(launches);
+  return cuda_status(e);
+}
+
+}  // extern "C"

@@ -276,6 +276,141 @@ saf3r_status saf3r_cache_export(const saf3r_layout* layout, const saf3r_head_cfg
 saf3r_status saf3r_kept_pairs(const saf3r_layout* layout, const saf3r_head_cfg* cfg, const void* cache,
                               int64_t* pairs, void* stream);
 
+/* ====================================================================== views taken one after another
+ *
+ * Streaming: the tokens of new views are rotated by their positions, their keys and values are
+ * appended to a paged cache, and their queries attend to the cached tokens.  No counterpart in the
+ * paper, which has all views in hand.  d = 64 throughout.
+ *
+ * Strides are in elements; a row's 64 values are contiguous.  Row starts must be 16-byte aligned
+ * (base pointers, and token and head strides a multiple of 8 for bf16 tensors, of 4 for fp32 ones).
+ * Strides may be in any order (token-major or head-major), but not negative.
+ */
+
+/* How the rotated dims of a head pair up. */
+typedef enum {
+    SAF3R_ROPE_HALF = 0,     /* each axis has its own dims[a] consecutive dims (axis 0 first), D = dims[a]:
+                                dims i and i + D/2 of them turn by pos[a] * base^(-2i/D) */
+    SAF3R_ROPE_PAIRS = 1,    /* the same, dims 2i and 2i + 1 */
+    SAF3R_ROPE_SECTIONS = 2  /* one rotation over the whole width R = sum of dims: dims j and j + R/2 turn by
+                                pos[axis(j)] * base^(-2j/R), the first dims[0]/2 values of j being axis 0's,
+                                the next dims[1]/2 axis 1's, and so on */
+} saf3r_rope_pairing;
+
+/* Rotary positions with several axes ((row, column) of images; (time, row, column) of videos).  A
+ * pair (a, b) that turns by the angle x becomes (a cos x - b sin x, a sin x + b cos x).  Dims from
+ * the sum of dims on are not rotated. */
+typedef struct {
+    int32_t n_axes;     /* 1..4 */
+    int32_t pairing;    /* saf3r_rope_pairing */
+    int32_t dims[4];    /* rotated dims of each axis: multiples of 8, >= 8; their sum at most 64 */
+    double base;        /* frequency base, 1 <= base <= 1e12 */
+} saf3r_rope_cfg;
+
+/*
+ * Rotate the first n_rot_heads heads of x by the tokens' positions and copy the others.
+ *   x, out: n_tokens x n_heads rows of 64 (bf16, or fp32 where *_is_fp32), rows of token t and head h at
+ *           t * token_stride + h * head_stride; out may be x itself (same type and strides), no
+ *           other overlap.  A projection's packed [token][q, k, v][head][64] rows are 3H heads of
+ *           which 2H are rotated, and head-major out strides give the [H][N][64] rows that the
+ *           attention calls take.
+ *   pos:    DEVICE int32 [n_tokens][n_axes], any value
+ *   inverse: nonzero turns by minus the angle: the adjoint, so the gradient of x from that of out
+ * Angles are exact to 2^-33 turns at every int32 position (64-bit fixed point); the rotation is in
+ * fp32 and rounded once.
+ */
+typedef struct {
+    int64_t n_tokens;
+    int32_t n_heads, n_rot_heads;
+    const void* x;
+    int64_t x_token_stride, x_head_stride;
+    void* out;
+    int64_t out_token_stride, out_head_stride;
+    int32_t x_is_fp32, out_is_fp32;
+    const int32_t* pos;
+    int32_t inverse;
+} saf3r_rope_args;
+saf3r_status saf3r_rope(const saf3r_rope_cfg* rope, const saf3r_rope_args* args, void* stream);
+
+/* Element types of a key/value cache. */
+typedef enum {
+    SAF3R_KV_BF16 = 0,
+    SAF3R_KV_E4M3 = 1   /* 8-bit floating point (4 exponent, 3 mantissa bits, largest 448); a value is
+                           code * scale, one fp32 scale for each (page, kv head) of keys and of values */
+} saf3r_kv_type;
+
+/*
+ * A paged cache of keys and values, in DEVICE memory of the caller: pools [n_pages][n_heads][page][64]
+ * and, for SAF3R_KV_E4M3, scales fp32 [n_pages][n_heads], always a power of two in 2^-100 .. 2^119.
+ * Nothing needs a start value.  Pools and scales 16-byte aligned.
+ */
+typedef struct {
+    int32_t n_pages;    /* >= 1 */
+    int32_t n_heads;    /* key/value heads, 1..64 */
+    int32_t page;       /* tokens of a page: 16, 32, 64 or 128 */
+    int32_t type;       /* saf3r_kv_type */
+    void* k;
+    void* v;
+    float* k_scale;     /* NULL for SAF3R_KV_BF16 */
+    float* v_scale;
+} saf3r_kv_cache;
+
+/*
+ * The new tokens of one step of several sequences (streams).  Sequence b has
+ * new = cu_tokens[b+1] - cu_tokens[b] new tokens: rows cu_tokens[b].. of the step's tensors, and
+ * tokens kv_lens[b] - new .. kv_lens[b] - 1 of the sequence.  Token i of it lives in row i % page of
+ * page page_table[b][i / page].  Arrays are DEVICE int32, read by the kernels: a captured graph
+ * follows their contents.  Rows behind the last sequence are not touched.  A sequence whose numbers
+ * do not fit (new < 0 or > max_new, rows outside 0 .. n_tokens, kv_lens > max_pages * page, kv_lens < new) or
+ * that needs a page outside the cache records SAF3R_ERR_INDEX: nothing is read or written outside the
+ * buffers, that sequence's results are unspecified.
+ */
+typedef struct {
+    int32_t n_seqs;     /* 0..65535 */
+    int32_t n_tokens;   /* rows of the step's tensors, >= 0 */
+    int32_t max_new;    /* the most new tokens of one sequence (a bound, for the launch), 0..n_tokens */
+    int32_t max_pages;  /* entries of a sequence's row of page_table */
+    const int32_t* cu_tokens;   /* [n_seqs + 1] */
+    const int32_t* kv_lens;     /* [n_seqs], with the new tokens */
+    const int32_t* page_table;  /* [n_seqs][max_pages]; entries of pages that no call needs may be anything */
+} saf3r_kv_batch;
+
+/* Key and value rows of a step: bf16, n_tokens x n_heads rows of 64. */
+typedef struct {
+    const void* k;
+    int64_t k_token_stride, k_head_stride;
+    const void* v;
+    int64_t v_token_stride, v_head_stride;
+    const int32_t* pos;   /* [n_tokens][n_axes] with a rope, else NULL */
+} saf3r_kv_rows;
+
+/*
+ * Append the new tokens' keys and values to the cache.
+ *   rope: keys are rotated on the way (fp32, rounded once to the cache's type); NULL: as they are.
+ *   SAF3R_KV_E4M3: of each (page, head), keys and values apart, the scale becomes
+ *     2^ceil(log2(m / 448)), m the largest finite magnitude among the new rows, but at least 2^-100, and not
+ *     less than the scale of the page's older rows when it has any; where that grew, the older rows' codes are
+ *     rounded again to the new scale (exact but for codes that become subnormal).  Codes are rounded to nearest,
+ *     ties to even; infinities and NaN become NaN.
+ * A page may take new rows of one sequence only; pages shared by sequences must be full.
+ */
+saf3r_status saf3r_kv_append(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch,
+                             const saf3r_rope_cfg* rope, const saf3r_kv_rows* rows, void* stream);
+
+/*
+ * Which tokens a query sees.  Tokens form views of view_tokens tokens in order (view_tokens 1: every token
+ * is its own view).  A query of view f sees
+ *   causal:      the views f - window + 1 .. f, and of the views 0 .. f the first n_sink tokens
+ *   not causal:  the views f - window + 1 .. f + window - 1, and the first n_sink tokens
+ * window 0: all views on those sides.  A token out of sight takes no part, whatever it holds.
+ */
+typedef struct {
+    int32_t view_tokens;  /* >= 1 */
+    int32_t window;       /* views, >= 0 */
+    int32_t n_sink;       /* tokens, >= 0 */
+    int32_t causal;
+} saf3r_window;
+
 /*
  * Timing hook for measurement: when start and stop are both non-NULL
  * cudaEvent_t handles, every following saf3r_sparse_attn / saf3r_dense_attn
