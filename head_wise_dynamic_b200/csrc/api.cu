@@ -701,6 +701,8 @@ bool saf3r::call_device(int* sms, int* major, int** err) {
   return true;
 }
 
+saf3r_status saf3r::validate_layout(const saf3r_layout* L) { return check_layout(L); }
+
 void saf3r::set_launch_count(int n) { t_launches = n; }
 
 long long saf3r::call_wait_budget() { return t_wait_budget; }

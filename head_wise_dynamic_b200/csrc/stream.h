@@ -60,16 +60,20 @@ struct WindowMask {
 };
 
 struct KvAttnParams {
-  KvView kv;
+  KvView kv;          // contiguous mode (ck != NULL): n_heads, n_seqs = 1, n_tokens, err only
   WindowMask win;
+  const uint16_t* ck;  // keys and values held at once, bf16 [heads][n_tokens][64] (NULL: the paged cache)
+  const uint16_t* cv;
   const uint16_t* q;
   void* out;
   long long q_ts, q_hs, out_ts, out_hs;
   int32_t n_heads, group, out_fp32;
+  int32_t e4m3;
   uint8_t* ws;
   int32_t num_sms;
   long long wait_budget;
   int32_t withhold;
+  int32_t n_split;     // decode: most pieces of one item
 };
 
 #ifdef __CUDACC__
@@ -81,6 +85,7 @@ struct SeqInfo {
 };
 __device__ __forceinline__ SeqInfo seq_info(const KvView& kv, int b) {
   SeqInfo s;
+  if (kv.cu == nullptr) return SeqInfo{0, kv.n_tokens, kv.n_tokens, true};  // views held at once
   s.row0 = kv.cu[b];
   const int end = kv.cu[b + 1];
   s.len = kv.kv_lens[b];
@@ -109,6 +114,16 @@ __device__ __forceinline__ Span span_of(const WindowMask& w, int p, int len) {
   return s;
 }
 
+// The same as two runs of keys in order: [0, a_end) and [b_begin, b_end).  For a tile of queries at positions
+// first..last: lo of the first, hi and sink of the last.
+struct Runs {
+  int a_end, b_begin, b_end;
+};
+__device__ __forceinline__ Runs runs_of(int lo, int hi, int sink) {
+  if (sink >= lo) return Runs{0, 0, max(hi, sink)};
+  return Runs{sink, lo, hi};
+}
+
 __device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int pos, float& s, float& c) {
   const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * t.freq[pair];
   // upper 32 bits as a signed fraction of a turn, in half turns: [-1, 1)
@@ -124,11 +139,16 @@ cudaError_t launch_append(const AppendParams& p, bool e4m3, int num_sms, cudaStr
 
 // few query rows per sequence and kv head (kv_decode.cu)
 bool decode_takes(int max_new, int group);
-size_t decode_workspace_bytes(const KvView& kv, const WindowMask& w, int n_heads, int num_sms);
-cudaError_t launch_decode(const KvAttnParams& p, bool e4m3, cudaStream_t stream, int* n_launch);
+size_t decode_workspace_bytes(const KvView& kv, const WindowMask& w, int group);
+cudaError_t launch_decode(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
+
+// the tensor-core kernel (kv_attn_sm100.cu)
+size_t attn_workspace_bytes(int n_seqs, int n_tokens, int n_heads);
+saf3r_status launch_attn(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
 
 // host side of api.cu that the streaming entry points share
 bool call_device(int* sms, int* major, int** err);
+saf3r_status validate_layout(const saf3r_layout* L);
 void set_launch_count(int n);
 long long call_wait_budget();
 bool take_withhold_arrive();

@@ -166,4 +166,101 @@ saf3r_status saf3r_kv_append(const saf3r_kv_cache* cache, const saf3r_kv_batch* 
   return cuda_status(e);
 }
 
+size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch,
+                                     const saf3r_window* window, int n_heads) {
+  if (check_cache(cache, false) != SAF3R_OK || check_batch(cache, batch, false) != SAF3R_OK || !window_ok(window) ||
+      n_heads < 1 || n_heads > kMaxHeads || n_heads % cache->n_heads)
+    return 0;
+  const KvView kv = view_of(cache, batch, nullptr);
+  const int group = n_heads / cache->n_heads;
+  const size_t n = decode_takes(batch->max_new, group)
+                       ? decode_workspace_bytes(kv, mask_of(window), group)
+                       : attn_workspace_bytes(batch->n_seqs, batch->n_tokens, n_heads);
+  return n < 256 ? 256 : n;
+}
+
+saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch, const saf3r_window* window,
+                           const saf3r_query_rows* rows, void* workspace, void* stream) {
+  set_launch_count(0);
+  saf3r_status st = check_cache(cache, true);
+  if (st != SAF3R_OK) return st;
+  if ((st = check_batch(cache, batch, true)) != SAF3R_OK) return st;
+  if (!window_ok(window) || !rows || rows->n_heads < 1 || rows->n_heads > kMaxHeads || rows->n_heads % cache->n_heads)
+    return SAF3R_ERR_INVALID;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0 || batch->max_new == 0) return SAF3R_OK;
+  if (!rows->q || !rows->out || !workspace || !aligned16(rows->q) || !aligned16(rows->out) || !aligned16(workspace))
+    return SAF3R_ERR_INVALID;
+  if (!strides_ok(batch->n_tokens, rows->q_token_stride, rows->n_heads, rows->q_head_stride, false, true) ||
+      !strides_ok(batch->n_tokens, rows->out_token_stride, rows->n_heads, rows->out_head_stride, rows->out_is_fp32 != 0,
+                  true))
+    return SAF3R_ERR_INVALID;
+  int sms = 0, *err = nullptr;
+  if ((st = device(&sms, &err)) != SAF3R_OK) return st;
+  KvAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = view_of(cache, batch, err);
+  p.win = mask_of(window);
+  p.q = static_cast<const uint16_t*>(rows->q);
+  p.out = rows->out;
+  p.q_ts = rows->q_token_stride;
+  p.q_hs = rows->q_head_stride;
+  p.out_ts = rows->out_token_stride;
+  p.out_hs = rows->out_head_stride;
+  p.n_heads = rows->n_heads;
+  p.group = rows->n_heads / cache->n_heads;
+  p.out_fp32 = rows->out_is_fp32 != 0;
+  p.e4m3 = cache->type == SAF3R_KV_E4M3;
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.num_sms = sms;
+  p.wait_budget = call_wait_budget();
+  int launches = 0;
+  if (decode_takes(batch->max_new, p.group))
+    st = cuda_status(launch_decode(p, static_cast<cudaStream_t>(stream), &launches));
+  else
+    st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
+  set_launch_count(launches);
+  return st;
+}
+
+size_t saf3r_window_attn_workspace_bytes(const saf3r_layout* layout, const saf3r_window* window) {
+  if (validate_layout(layout) != SAF3R_OK || !window_ok(window)) return 0;
+  return attn_workspace_bytes(1, make_dims(*layout).N, layout->H);
+}
+
+saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* window, const void* q, const void* k,
+                               const void* v, void* out, int out_is_fp32, void* workspace, void* stream) {
+  set_launch_count(0);
+  saf3r_status st = validate_layout(layout);
+  if (st != SAF3R_OK) return st;
+  if (!window_ok(window) || !q || !k || !v || !out || !workspace || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(out) || !aligned16(workspace))
+    return SAF3R_ERR_INVALID;
+  int sms = 0, *err = nullptr;
+  if ((st = device(&sms, &err)) != SAF3R_OK) return st;
+  const Dims d = make_dims(*layout);
+  KvAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv.err = err;
+  p.kv.n_heads = d.H;
+  p.kv.n_seqs = 1;
+  p.kv.n_tokens = p.kv.max_new = d.N;
+  p.win = mask_of(window);
+  p.ck = static_cast<const uint16_t*>(k);
+  p.cv = static_cast<const uint16_t*>(v);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = out;
+  p.q_ts = p.out_ts = kD;
+  p.q_hs = p.out_hs = static_cast<long long>(d.N) * kD;
+  p.n_heads = d.H;
+  p.group = 1;
+  p.out_fp32 = out_is_fp32 != 0;
+  p.ws = static_cast<uint8_t*>(workspace);
+  p.num_sms = sms;
+  p.wait_budget = call_wait_budget();
+  int launches = 0;
+  st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
+  set_launch_count(launches);
+  return st;
+}
+
 }  // extern "C"

@@ -13,7 +13,8 @@ from typing import Optional, Sequence
 import head_wise_dynamic_b200 as _hw
 
 __all__ = ["ROPE_HALF", "ROPE_PAIRS", "ROPE_SECTIONS", "KV_BF16", "KV_E4M3", "make_rope", "PagedKV", "KVBatch",
-           "saf3r_rope", "saf3r_kv_append"]
+           "make_window", "saf3r_rope", "saf3r_kv_append", "saf3r_kv_attn", "saf3r_kv_attn_workspace_bytes",
+           "saf3r_window_attn", "saf3r_window_attn_workspace_bytes"]
 
 # saf3r_rope_pairing
 ROPE_HALF, ROPE_PAIRS, ROPE_SECTIONS = range(3)
@@ -64,8 +65,14 @@ def declare(L) -> None:
     P = ctypes.POINTER
     L.saf3r_rope.argtypes = [P(saf3r_rope_cfg), P(saf3r_rope_args), _vp]
     L.saf3r_kv_append.argtypes = [P(saf3r_kv_cache), P(saf3r_kv_batch), P(saf3r_rope_cfg), P(saf3r_kv_rows), _vp]
-    for f in (L.saf3r_rope, L.saf3r_kv_append):
+    L.saf3r_kv_attn.argtypes = [P(saf3r_kv_cache), P(saf3r_kv_batch), P(saf3r_window), P(saf3r_query_rows), _vp, _vp]
+    L.saf3r_window_attn.argtypes = [P(_hw.saf3r_layout), P(saf3r_window), _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _vp]
+    for f in (L.saf3r_rope, L.saf3r_kv_append, L.saf3r_kv_attn, L.saf3r_window_attn):
         f.restype = ctypes.c_int
+    L.saf3r_kv_attn_workspace_bytes.argtypes = [P(saf3r_kv_cache), P(saf3r_kv_batch), P(saf3r_window), ctypes.c_int]
+    L.saf3r_window_attn_workspace_bytes.argtypes = [P(_hw.saf3r_layout), P(saf3r_window)]
+    for f in (L.saf3r_kv_attn_workspace_bytes, L.saf3r_window_attn_workspace_bytes):
+        f.restype = ctypes.c_size_t
 
 
 # ------------------------------------------------------------------ configurations
@@ -106,6 +113,11 @@ def _row_strides(t, tokens: int, heads: int, device, what: str):
     _need(c == 1, f"{what}: the last dimension must be contiguous")
     # the stride of a dimension of one says nothing: any valid one will do
     return (a if tokens > 1 else 64), (b if heads > 1 else 64)
+
+
+def _workspace(t, n: int, device):
+    _need(t.is_contiguous() and t.device == device and t.numel() * t.element_size() >= n,
+          f"workspace: a contiguous tensor of at least {n} bytes on {device} is wanted")
 
 
 class _on:
@@ -217,3 +229,47 @@ def saf3r_kv_append(cache: PagedKV, batch: KVBatch, k, v, rope=None, pos=None, s
     with _on(dev, stream) as st:
         _hw._check(_hw.lib().saf3r_kv_append(_ref(cache.c), _ref(batch.c), None if rope is None else _ref(rope),
                                              _ref(a), st), "saf3r_kv_append")
+
+
+def saf3r_kv_attn_workspace_bytes(cache: PagedKV, batch: KVBatch, window: saf3r_window, n_heads: int) -> int:
+    """Workspace bytes of saf3r_kv_attn for n_heads query heads (ValueError for sizes it does not take)."""
+    n = int(_hw.lib().saf3r_kv_attn_workspace_bytes(_ref(cache.c), _ref(batch.c), _ref(window), int(n_heads)))
+    _need(n > 0, "sizes that saf3r_kv_attn does not take")
+    return n
+
+
+def saf3r_kv_attn(cache: PagedKV, batch: KVBatch, window: saf3r_window, q, out, workspace, stream=None):
+    """Attention of the step's queries q [n_tokens, heads, 64] (bf16) over the cache, which holds the step's
+    keys and values already, into out [n_tokens, heads, 64] (bf16 or fp32); rows in any order."""
+    import torch
+    dev, T, H = cache.device, batch.n_tokens, q.shape[1]
+    fp32 = out.dtype == torch.float32
+    _need(batch.device == dev and q.dtype == torch.bfloat16 and (fp32 or out.dtype == torch.bfloat16),
+          "q: bfloat16, out: bfloat16 or float32, the batch on the cache's device")
+    qs, os = _row_strides(q, T, H, dev, "q"), _row_strides(out, T, H, dev, "out")
+    _workspace(workspace, saf3r_kv_attn_workspace_bytes(cache, batch, window, H), dev)
+    a = saf3r_query_rows(H, int(fp32), q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1])
+    with _on(dev, stream) as st:
+        _hw._check(_hw.lib().saf3r_kv_attn(_ref(cache.c), _ref(batch.c), _ref(window), _ref(a), workspace.data_ptr(), st),
+                   "saf3r_kv_attn")
+
+
+def saf3r_window_attn_workspace_bytes(layout, window: saf3r_window) -> int:
+    n = int(_hw.lib().saf3r_window_attn_workspace_bytes(_ref(_hw.layout_of(layout)), _ref(window)))
+    _need(n > 0, "a layout or window that saf3r_window_attn does not take")
+    return n
+
+
+def saf3r_window_attn(layout, window: saf3r_window, q, k, v, out, workspace, stream=None):
+    """Attention with a sliding window of views and sinks over q, k, v [H, N, 64] (bf16) held at once,
+    into out [H, N, 64] (bf16 or fp32)."""
+    import torch
+    L = _hw.layout_of(layout)
+    dev, shape = q.device, (L.H, L.S * (L.grid_h * L.grid_w + L.n_special), L.d)
+    fp32 = out.dtype == torch.float32
+    ptrs = [_dense(t, torch.bfloat16, shape, dev, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    ptrs.append(_dense(out, torch.float32 if fp32 else torch.bfloat16, shape, dev, "out"))
+    _workspace(workspace, saf3r_window_attn_workspace_bytes(L, window), dev)
+    with _on(dev, stream) as st:
+        _hw._check(_hw.lib().saf3r_window_attn(_ref(L), _ref(window), *ptrs, int(fp32), workspace.data_ptr(), st),
+                   "saf3r_window_attn")

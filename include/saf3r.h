@@ -411,6 +411,41 @@ typedef struct {
     int32_t causal;
 } saf3r_window;
 
+/* Query and output rows of a step. */
+typedef struct {
+    int32_t n_heads;      /* query heads, 1..64, a multiple of the cache's heads: head h reads kv head h / (n_heads / kv heads) */
+    int32_t out_is_fp32;
+    const void* q;        /* bf16, n_tokens x n_heads rows of 64 */
+    int64_t q_token_stride, q_head_stride;
+    void* out;            /* bf16 or fp32 */
+    int64_t out_token_stride, out_head_stride;
+} saf3r_query_rows;
+
+/* Workspace bytes of saf3r_kv_attn for these sizes (pointers are not read; 0 for invalid arguments). */
+size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch,
+                                     const saf3r_window* window, int n_heads);
+
+/*
+ * Attention of each sequence's new tokens to its cached tokens, themselves among them (append first):
+ * softmax(q . k / sqrt(64)) over the tokens that `window` lets them see.  Pages without a visible token are not
+ * read: the caller may have given them to others.  Few rows per sequence (max_new * heads per kv head up to a limit)
+ * take a kernel that splits the keys over the GPU; others the tensor-core kernel.
+ * workspace: DEVICE, 16-byte aligned, saf3r_kv_attn_workspace_bytes bytes, used by one call at a time
+ * (also when calls are captured: graphs that share it must not overlap); it needs no start value.
+ */
+saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch, const saf3r_window* window,
+                           const saf3r_query_rows* rows, void* workspace, void* stream);
+
+/* Workspace bytes of saf3r_window_attn (0 for invalid arguments). */
+size_t saf3r_window_attn_workspace_bytes(const saf3r_layout* layout, const saf3r_window* window);
+
+/*
+ * Attention over views held at once, q, k, v and out as saf3r_dense_attn, each token seeing what `window`
+ * says (view_tokens is usually the layout's V, but need not be).  Workspace as saf3r_kv_attn.
+ */
+saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* window, const void* q, const void* k,
+                               const void* v, void* out, int out_is_fp32, void* workspace, void* stream);
+
 /*
  * Timing hook for measurement: when start and stop are both non-NULL
  * cudaEvent_t handles, every following saf3r_sparse_attn / saf3r_dense_attn
