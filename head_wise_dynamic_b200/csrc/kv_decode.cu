@@ -54,28 +54,6 @@ __device__ __forceinline__ T load_stream(const void* p) {
   return __ldcs(static_cast<const T*>(p));
 }
 
-// The pieces of one item.  cps chunks make a piece, chosen so that all items' pieces together fill
-// the GPU a few times over, from the sequences' actual lengths.
-struct Pieces {
-  int n;        // pieces of this item
-  int begin;    // chunk range of piece `s`
-  int end;
-};
-
-// Chunks (64 keys, from multiples of 64) that rows at positions first..last touch.
-struct Chunks {
-  int na, b0, total;
-  __device__ __forceinline__ int key(int i) const { return (i < na ? i : i - na + b0) << 6; }
-};
-__device__ __forceinline__ Chunks chunks_of(const Runs& r) {
-  Chunks c;
-  c.na = (r.a_end + 63) >> 6;
-  c.b0 = r.b_begin >> 6;
-  if (c.b0 < c.na) c.na = 0, c.b0 = 0;  // the runs share a chunk
-  c.total = c.na + (r.b_end > r.b_begin ? ((r.b_end + 63) >> 6) - c.b0 : 0);
-  return c;
-}
-
 // Chunks of a whole sequence's new tokens (what its items read, at most).
 __device__ __forceinline__ int seq_chunks(const WindowMask& w, const SeqInfo& s) {
   if (s.n_new <= 0) return 0;
@@ -160,7 +138,8 @@ __device__ __forceinline__ void store_row(const KvAttnParams& p, const Item& it,
 __device__ __forceinline__ void exact_item(const KvAttnParams& p, const Item& it, int warp, int lane) {
   for (int r = warp; r < it.rows; r += kWarps) {
     const int i = it.r0 + r, tok = i / p.group;
-    exact_row(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i % p.group, lane);
+    exact_row(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i % p.group, lane, 0,
+              kD);
   }
 }
 

@@ -124,6 +124,20 @@ __device__ __forceinline__ Runs runs_of(int lo, int hi, int sink) {
   return Runs{sink, lo, hi};
 }
 
+// The chunks (64 keys, from multiples of 64) that two runs touch, in order.
+struct Chunks {
+  int na, b0, total;
+  __device__ __forceinline__ int key(int i) const { return (i < na ? i : i - na + b0) << 6; }
+};
+__device__ __forceinline__ Chunks chunks_of(const Runs& r) {
+  Chunks c;
+  c.na = (r.a_end + 63) >> 6;
+  c.b0 = r.b_begin >> 6;
+  if (c.b0 < c.na) c.na = 0, c.b0 = 0;  // the runs share a chunk
+  c.total = c.na + (r.b_end > r.b_begin ? ((r.b_end + 63) >> 6) - c.b0 : 0);
+  return c;
+}
+
 __device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int pos, float& s, float& c) {
   const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * t.freq[pair];
   // upper 32 bits as a signed fraction of a turn, in half turns: [-1, 1)
@@ -143,8 +157,8 @@ size_t decode_workspace_bytes(const KvView& kv, const WindowMask& w, int group);
 cudaError_t launch_decode(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
 
 // the tensor-core kernel (kv_attn_sm100.cu)
-size_t attn_workspace_bytes(int n_seqs, int n_tokens, int n_heads);
-saf3r_status launch_attn(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
+size_t attn_workspace_bytes();
+cudaError_t launch_attn(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
 
 // host side of api.cu that the streaming entry points share
 bool call_device(int* sms, int* major, int** err);

@@ -175,7 +175,7 @@ size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv
   const int group = n_heads / cache->n_heads;
   const size_t n = decode_takes(batch->max_new, group)
                        ? decode_workspace_bytes(kv, mask_of(window), group)
-                       : attn_workspace_bytes(batch->n_seqs, batch->n_tokens, n_heads);
+                       : attn_workspace_bytes();
   return n < 256 ? 256 : n;
 }
 
@@ -216,15 +216,17 @@ saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* ba
   int launches = 0;
   if (decode_takes(batch->max_new, p.group))
     st = cuda_status(launch_decode(p, static_cast<cudaStream_t>(stream), &launches));
-  else
-    st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
+  else {
+    p.withhold = take_withhold_arrive();
+    st = cuda_status(launch_attn(p, static_cast<cudaStream_t>(stream), &launches));
+  }
   set_launch_count(launches);
   return st;
 }
 
 size_t saf3r_window_attn_workspace_bytes(const saf3r_layout* layout, const saf3r_window* window) {
   if (validate_layout(layout) != SAF3R_OK || !window_ok(window)) return 0;
-  return attn_workspace_bytes(1, make_dims(*layout).N, layout->H);
+  return attn_workspace_bytes();
 }
 
 saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* window, const void* q, const void* k,
@@ -257,8 +259,9 @@ saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* w
   p.ws = static_cast<uint8_t*>(workspace);
   p.num_sms = sms;
   p.wait_budget = call_wait_budget();
+  p.withhold = take_withhold_arrive();
   int launches = 0;
-  st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
+  st = cuda_status(launch_attn(p, static_cast<cudaStream_t>(stream), &launches));
   set_launch_count(launches);
   return st;
 }

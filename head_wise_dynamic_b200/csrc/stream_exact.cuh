@@ -27,8 +27,9 @@ __device__ __forceinline__ long long kv_row(const KvAttnParams& p, int b, int hk
   return ((*scale << kv.page_log2) + (j & (kv.page - 1))) * kD;
 }
 
-// Run by one warp: token `row` of the step's tensors, at position pos of sequence b.
-__device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int len, int row, int pos, int head, int lane) {
+// Run by one warp: token `row` of the step's tensors, at position pos of sequence b.  Writes columns c0..c1-1.
+static __device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int len, int row, int pos, int head, int lane, int c0,
+                                       int c1) {
   const int hk = head / p.group;
   const Span sp = span_of(p.win, pos, len);
   const uint16_t* q = p.q + row * p.q_ts + head * p.q_hs;
@@ -88,6 +89,7 @@ __device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int len, in
   const float inv = l == 0.f ? 0.f : 1.f / l;
   a0 *= inv;
   a1 *= inv;
+  if (2 * lane < c0 || 2 * lane >= c1) return;
   const long long o = row * p.out_ts + head * p.out_hs + 2 * lane;
   if (p.out_fp32) {
     static_cast<float*>(p.out)[o] = a0;
