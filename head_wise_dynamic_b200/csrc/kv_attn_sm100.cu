@@ -8,20 +8,22 @@
 // keep every SM busy with few items (one view of one stream: 96 items of unequal length on 148 SMs).
 //
 // Warps (20):
-//   0-2    loaders: copy (bf16) or convert (8-bit) each block's K and V rows into a ring of kStages stages, in the
-//          128-byte-swizzled layout that the tensor core reads.  Rows that no row of the item sees are zero, so
-//          what lies behind a sequence's end or in another's page never enters.  An 8-bit code times its page's
-//          power-of-two scale is a bf16 value exactly (4 significant bits, the exponent within bf16's), so the products
-//          are the bf16 ones in both cases.
+//   0-1    loaders: each block's K and V rows into a ring of stages, in the 128-byte-swizzled layout that the tensor
+//          core reads, a TMA box for each page (or 64 rows of it).  Value rows that no row of the item sees are cleared:
+//          what lies behind a sequence's end need not be finite.  bf16: TMA writes the stage itself.  8-bit: the
+//          codes land beside it and become fp16 (exact, one conversion for two).  The page's key scale multiplies the fp32
+//          logits; its value scale goes into the exponent, so that P is the weight times it; the row's sum takes
+//          it out again.
+//   2-3    issue the products, a warp for each tile.
 //   4-19   softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
-//          Sixteen warps, four for each scheduler in different steps of two tiles, hide each other's waits.
-//   3      issues the products.
-// Tensor memory (512 columns): for each tile S (128 fp32 columns; each half's bf16 P goes over the first 32 columns of
-// its half once read) and an accumulator O for each key half (64 columns).  The halves have a running
-// maximum and sum of their own and meet when the piece ends.
+//          Sixteen warps, four for each scheduler in different steps, hide each other's waits.
+// Tensor memory (512 columns): for each tile S (128 fp32 columns; each half's P, bf16 or fp16, goes over the first 32
+// columns of its half once read) and an accumulator O for each key half (64 columns).  The halves have a
+// reference and sum of their own and meet when the piece ends.
 //
-// A row's reference maximum moves only when a block exceeds it by 2^8: bf16 P and the fp32 sums
-// keep their relative precision at any reference, so the answer does not depend on it.
+// Weights are 2^(x - reference), the reference a row's largest logit of its first block: bf16 P and the fp32 sums
+// keep their relative precision at any reference, so no maximum is taken of later blocks.  Only a block whose
+// weights sum to more than 2^24 moves it: its logits are read again, what was summed so far is scaled.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -36,23 +38,29 @@ namespace saf3r {
 
 namespace {
 
-constexpr int kLoaders = 3;            // warps
-constexpr int kThreads = 640;
-constexpr int kStages = 3;
-constexpr int kRaw = 3;
+constexpr int kConverters = 4;         // warps that convert 8-bit codes
+constexpr int kScales = 8;             // blocks whose scales are kept: 3 raw ones and the 3 stages'
+constexpr int kMaxStages = 4;
+constexpr int kPieces = 4;             // pieces that warp 0 may be ahead
 constexpr int kItem = 256;             // rows of an item
 constexpr int kRowBytes = 128;
 constexpr int kBlockBytes = 128 * kRowBytes;  // 128 rows x 64 bf16
 constexpr float kScaleLog2 = 0.18033688011112042f;  // log2(e) / sqrt(64)
-constexpr float kGrow = 8.0f;
+constexpr float kGrow = 16777216.f;    // a block's weights may sum to 2^24 before its rows' references move
+constexpr float kGrowF16 = 8192.f;     // fp16 P: within its range,
+constexpr float kF16Head = 6.f;        // and a first block's largest weight is 2^6, so that fp16 ends 2^-30 below it
+constexpr int kWild = 64;              // largest spread of value scales (in exponents) that P's fp32 sum is sure to bear
 constexpr int kMaxShares = 160;        // CTAs of a launch at most (one for each SM)
 constexpr int kPlanEntries = 1024;
-// Cost of a key block and of an item's start and end, in eighths of a two-tile block.
-constexpr int kCost2 = 8, kCost1 = 5, kCostItem = 8;
+// Cost of a key block and of an item's start and end, in sixteenths of a two-tile block.
+constexpr int kCost2 = 16, kCost1 = 13, kCostItem = 16;
 constexpr int kLeastShare = 4 * kCost2;  // shares smaller than this are not worth a CTA
 
 // Pairs (of the 32 of a row's 64 keys) whose exponentials run on the FMA pipe.
-constexpr uint32_t kPolyPairs = 0x88888888u;
+#ifndef POLY
+#define POLY 0x88888888u
+#endif
+constexpr uint32_t kPolyPairs = POLY;
 // p(f) = 1 + f (c1 + f (c2 + f c3)), fitted to 2^f on [0, 1) for least maximum relative error (8.6e-5)
 constexpr float kExpC1 = 0.6951168179512024f, kExpC2 = 0.22764486074447632f, kExpC3 = 0.07706713676452637f;
 
@@ -127,17 +135,36 @@ struct Plan {
   int shares;
 };
 
+// Scales of a chunk's four groups of 16 keys: of the keys, log2 of the values' and one over the values'.
+struct alignas(16) ChunkScale {
+  float k[4], lv[4], vi[4];
+};
+
+// The ring of key blocks (stages of 128 rows of K, then of V) and, for 8-bit caches, the raw blocks behind it.
+template <bool kE4m3>
+struct Ring {
+  static constexpr int kWarps = kE4m3 ? 24 : 20, kSoftmax = kWarps - 16;  // warps, the first softmax warp
+  static constexpr int kStages = kE4m3 ? 3 : 4, kRaw = kE4m3 ? 3 : 0;
+  static constexpr int kBytes = (2 * kStages + kRaw) * kBlockBytes;
+};
+constexpr int kRingBytes = Ring<true>::kBytes > Ring<false>::kBytes ? Ring<true>::kBytes : Ring<false>::kBytes;
+
 struct AttnSmem {
   uint8_t q[2][2][kBlockBytes];
-  uint8_t kv[kStages][2 * kBlockBytes];  // 128 rows of K, then of V
-  uint8_t raw[kRaw][kBlockBytes];        // 8-bit caches: 128 rows of 64 codes of K, then of V
-  uint64_t full[kStages], empty[kStages];
-  uint64_t q_empty[2];
-  uint64_t s_full[2], o_done[2], p_full[2][2];
-  uint64_t drain;
+  uint8_t ring[kRingBytes];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t raw[kMaxStages], raw_empty[kMaxStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2][2], o_done[2], p_full[2][2];
+  uint64_t drain[2];
   uint64_t pair[2][4];                // the two warps of a tile's 32 rows meet here
-  float stats[2][2][2][128][2];       // [piece parity][tile][half][row] = (maximum, sum)
+  float stats[2][2][2][128][2];       // [piece parity][tile][half][row] = (reference, sum)
+  ChunkScale scale[kScales][2];       // 8-bit: scales of a block's chunks
+  float q_scale[kPieces][kItem][2];         // 8-bit: what a row's logits are multiplied by
+  int wild[kPieces];                  // 8-bit: the piece's value scales are too far apart for P
   Plan plan;
+  Piece pieces[kPieces];              // warp 0's walk, for the other warps; blk1 < 0: the end
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem_base;
   int abort;
 };
@@ -162,7 +189,7 @@ __device__ void make_plan(const KvAttnParams& p, Plan& plan, long long* entries)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.kv.n_seqs + kPlanEntries - 1) / kPlanEntries;
   const int n = (p.kv.n_seqs + per - 1) / per;
-  for (int e = warp; e < n; e += kThreads / 32) {
+  for (int e = warp; e < n; e += blockDim.x / 32) {
     long long c = 0;
     for (int b = e * per; b < min((e + 1) * per, p.kv.n_seqs); ++b) c += seq_cost(p, b, lane);
     if (lane == 0) entries[e] = c;
@@ -255,7 +282,7 @@ __device__ void make_plan(const KvAttnParams& p, Plan& plan, long long* entries)
   }
 }
 
-// Walks the pieces of this CTA's share; every role walks for itself.
+// Walks the pieces of this CTA's share (warp 0).
 struct Walk {
   long long x, xs, xe;
   int hk, b, tile;
@@ -298,18 +325,62 @@ struct Walk {
   }
 };
 
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 __device__ __forceinline__ bool wait_all(const KvAttnParams& p, AttnSmem& sm, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, &sm.abort, p.kv.err, p.wait_budget, SAF3R_ERR_TIMEOUT));
 }
 
+// The other warps' view of the walk.
+struct Feed {
+  uint32_t i = 0;
+  __device__ __forceinline__ const Piece* next(const KvAttnParams& p, AttnSmem& sm) const {
+    if (!wait_all(p, sm, &sm.piece_full[i % kPieces], (i / kPieces) & 1)) return nullptr;
+    const Piece* pc = &sm.pieces[i % kPieces];
+    return pc->blk1 < 0 ? nullptr : pc;
+  }
+  __device__ __forceinline__ void done(AttnSmem& sm, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.piece_empty[i % kPieces]);
+    ++i;
+  }
+};
+// Warp 0 hands piece number i to the others (pc.blk1 < 0: there are no more).
+__device__ __forceinline__ bool publish(const KvAttnParams& p, AttnSmem& sm, uint32_t i, const Piece& pc, int lane) {
+  if (i >= kPieces && !wait_all(p, sm, &sm.piece_empty[i % kPieces], ((i / kPieces) & 1) ^ 1)) return false;
+  if (lane == 0) {
+    sm.pieces[i % kPieces] = pc;
+    mbar_arrive(&sm.piece_full[i % kPieces]);
+  }
+  __syncwarp();
+  return true;
+}
+
 // ------------------------------------------------------------------ loaders
 
-// First row in the pools (or in ck, cv) of the 16 keys from key j of the piece, -1: none of them is read.
-__device__ __forceinline__ int group_row(const KvAttnParams& p, const Piece& pc, int j) {
-  if (!(j < pc.runs.b_end && (j + 16 > pc.runs.b_begin || j < pc.runs.a_end))) return -1;
+// First key of this lane's box (2^box_log2 keys) of a block, -1: there is none, or no row sees a key of it.
+__device__ __forceinline__ int box_key(const KvAttnParams& p, const Piece& pc, int blk, int lane) {
+  const int i = lane << p.box_log2, c = 2 * blk + (i >> 6);
+  if (i >= 128 || c >= pc.ch.total || blk >= pc.blk1) return -1;
+  const int j = pc.ch.key(c) + (i & 63);
+  return j < pc.runs.b_end && (j + (1 << p.box_log2) > pc.runs.b_begin || j < pc.runs.a_end) ? j : -1;
+}
+
+// Its entry of the page table (used a block later, so that the load's latency is out of the way).
+__device__ __forceinline__ int box_entry(const KvAttnParams& p, const Piece& pc, int blk, int lane) {
+  const int j = box_key(p, pc, blk, lane);
+  if (j < 0 || p.ck) return 0;
+  return p.kv.table[static_cast<long long>(pc.b) * p.kv.max_pages + (j >> p.kv.page_log2)];
+}
+
+// Its first row in the pools (views held at once: in the head), -1: not read, or the page is not there.
+__device__ __forceinline__ int box_row(const KvAttnParams& p, const Piece& pc, int blk, int lane, int id) {
   const KvView& kv = p.kv;
-  if (p.ck) return pc.hk * kv.n_tokens + j;
-  const int id = kv.table[static_cast<long long>(pc.b) * kv.max_pages + (j >> kv.page_log2)];
+  const int j = box_key(p, pc, blk, lane);
+  if (j < 0) return -1;
+  if (p.ck) return j;
   if (id < 0 || id >= kv.n_pages) {
     atomicCAS(kv.err, 0, SAF3R_ERR_INDEX);
     return -1;
@@ -319,253 +390,311 @@ __device__ __forceinline__ int group_row(const KvAttnParams& p, const Piece& pc,
 
 __device__ __forceinline__ bool seen_by_some(const Runs& r, int j) { return j < r.b_end && (j >= r.b_begin || j < r.a_end); }
 
-// Key of group g (16 keys) of block `blk`, and whether the chunk exists.
-__device__ __forceinline__ int group_key(const Piece& pc, int blk, int g) {
-  const int i = 2 * blk + (g >> 2);
-  return i < pc.ch.total ? pc.ch.key(i) + 16 * (g & 3) : -1;
+// Whether some row of the item sees every key of the block.
+__device__ __forceinline__ bool whole_block(const Piece& pc, int blk) {
+  if (2 * blk + 1 >= pc.ch.total) return false;
+  const int a = pc.ch.key(2 * blk), b = pc.ch.key(2 * blk + 1);
+  return (a + 64 <= pc.runs.a_end || (a >= pc.runs.b_begin && a + 64 <= pc.runs.b_end)) &&
+         (b + 64 <= pc.runs.a_end || (b >= pc.runs.b_begin && b + 64 <= pc.runs.b_end));
 }
 
-// A block's copies are cut into units of one instruction of a warp, dealt to the kLoaders warps in turn.
-__device__ __forceinline__ void load_q(const KvAttnParams& p, AttnSmem& sm, const Piece& pc, int buf, int warp, int lane) {
-  const int col = lane & 7;
-#pragma unroll 2
-  for (int u = warp; u < kItem / 4; u += kLoaders) {
-    const int r = 4 * u + (lane >> 3), a = pc.row0 + r;
-    const bool have = r < pc.rows;
-    const int tok = a / p.group, head = pc.hk * p.group + a - tok * p.group;
-    const uint16_t* src = have ? p.q + (pc.s.row0 + tok) * p.q_ts + head * p.q_hs + col * 8 : p.q;
-    cp_async16(smem_u32(sm.q[buf][r >> 7]) + (r & 127) * kRowBytes + ((col ^ (r & 7)) << 4), src, have ? 16u : 0u);
+// A block's boxes of K and V into `dst` (64 rows of a chunk after the other, K then V); run by a warp, one lane a box.
+__device__ __forceinline__ void issue_boxes(const KvAttnParams& p, const CUtensorMap* mk, const CUtensorMap* mv, const Piece& pc,
+                                            int row, uint8_t* dst, uint64_t* bar, int row_bytes, int lane) {
+  const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+  if (lane == 0) mbar_arrive_expect_tx(bar, ((2 * __popc(have)) << p.box_log2) * row_bytes);
+  __syncwarp();
+  if (row >= 0) {
+    const int head = p.ck ? pc.hk : 0;
+    uint8_t* d = dst + (lane << p.box_log2) * row_bytes;
+    tma_load_3d(d, mk, 0, row, head, bar);
+    tma_load_3d(d + 128 * row_bytes, mv, 0, row, head, bar);
   }
+  __syncwarp();
 }
 
-__device__ __forceinline__ void loader_bf16(const KvAttnParams& p, AttnSmem& sm, int warp, int lane) {
-  const int col = lane & 7, rr = lane >> 3;
-  const uint16_t* kp = (p.ck ? p.ck : reinterpret_cast<const uint16_t*>(p.kv.k)) + col * 8;
-  const uint16_t* vp = (p.ck ? p.cv : reinterpret_cast<const uint16_t*>(p.kv.v)) + col * 8;
+// bf16, warp 0: every block's TMA boxes, straight into its stage.  Blocks that no row sees all of land on `raw` first,
+// for warp 1 to clear the values out of sight.
+__device__ __forceinline__ void load_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
+  constexpr int kStages = Ring<false>::kStages;
   Walk w(p, sm.plan);
   Piece pc;
-  uint32_t n = 0, pieces = 0;
+  uint32_t n = 0, raw = 0, last_raw = 0;  // bit st: parity of raw[st]; whether the stage's last block was a partial one
+  uint32_t pieces = 0;
   bool ok = true;
   while (ok && w.next(p, pc)) {
-    const int buf = pieces & 1;
-    if (pieces >= 2 && !wait_all(p, sm, &sm.q_empty[buf], ((pieces >> 1) - 1) & 1)) break;
+    if (!publish(p, sm, pieces, pc, lane)) {
+      ok = false;
+      break;
+    }
     ++pieces;
-    load_q(p, sm, pc, buf, warp, lane);
-    auto rows_of = [&](int blk) {  // lane g < 8: the first row of the block's group g
-      const int j = lane < 8 && blk < pc.blk1 ? group_key(pc, blk, lane) : -1;
-      return j >= 0 ? group_row(p, pc, j) : -1;
-    };
-    int base = rows_of(pc.blk0);
-    int pend = -1;
+    int entry = box_entry(p, pc, pc.blk0, lane);
     for (int blk = pc.blk0; blk < pc.blk1; ++blk, ++n) {
-      const int next = rows_of(blk + 1);
+      const int row = box_row(p, pc, blk, lane, entry);
+      entry = box_entry(p, pc, blk + 1, lane);
       const uint32_t st = n % kStages;
       if (n >= kStages && !wait_all(p, sm, &sm.empty[st], ((n / kStages) & 1) ^ 1)) {
         ok = false;
         break;
       }
-      const uint32_t kd = smem_u32(sm.kv[st]);
-      const int key0 = pc.ch.key(2 * blk), key1 = 2 * blk + 1 < pc.ch.total ? pc.ch.key(2 * blk + 1) : INT_MAX - 64;
-#pragma unroll 4
-      for (int u = warp; u < 32; u += kLoaders) {  // four rows of K and of V
-        const int r = 4 * u + rr;
-        const int row = __shfl_sync(0xffffffffu, base, u >> 2);
-        const bool have = row >= 0 && seen_by_some(pc.runs, (r < 64 ? key0 : key1 - 64) + r);
-        const long long at = have ? static_cast<long long>(row + (r & 15)) * kD : 0;
-        const uint32_t dst = kd + r * kRowBytes + ((col ^ (r & 7)) << 4);
-        cp_async16(dst, kp + at, have ? 16u : 0u);
-        cp_async16(dst + kBlockBytes, vp + at, have ? 16u : 0u);
-      }
-      cp_async_commit();
-      if (pend >= 0) {
-        cp_async_wait<1>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.full[pend]);
-      }
-      pend = static_cast<int>(st);
-      base = next;
+      const bool whole = whole_block(pc, blk);
+      issue_boxes(p, mk, mv, pc, row, sm.ring + st * 2 * kBlockBytes, whole ? &sm.full[st] : &sm.raw[st], kRowBytes, lane);
+      if (lane == 0) mbar_arrive(&sm.full[st]);
+      raw ^= (whole ? 0u : 1u) << st;
+      last_raw = (last_raw & ~(1u << st)) | ((whole ? 0u : 1u) << st);
     }
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (pend >= 0 && lane == 0) mbar_arrive(&sm.full[pend]);
   }
-  cp_async_wait<0>();
+  pc.blk1 = -1;
+  if (ok) publish(p, sm, pieces, pc, lane);
+  // every copy has landed before the block exits
+  for (uint32_t c = n > kStages ? n - kStages : 0; c < n; ++c) {
+    const uint32_t st = c % kStages;
+    if ((last_raw >> st) & 1u)
+      mbar_wait_drain(&sm.raw[st], ((raw >> st) & 1u) ^ 1u, kDrainBudget);
+    else
+      mbar_wait_drain(&sm.full[st], (c / kStages) & 1, kDrainBudget);
+  }
 }
 
-// two codes as the bf16 values that they stand for
-__device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t two, float scale) {
+// bf16, warp 1: zeros over the values of partial blocks that no row sees (what lies there need not be finite).
+__device__ __forceinline__ void clear_role(const KvAttnParams& p, AttnSmem& sm, int lane) {
+  constexpr int kStages = Ring<false>::kStages;
+  Feed feed;
+  uint32_t n = 0, raw = 0;
+  while (const Piece* next = feed.next(p, sm)) {
+    const Piece& pc = *next;
+    for (int blk = pc.blk0; blk < pc.blk1; ++blk, ++n) {
+      if (whole_block(pc, blk)) continue;
+      const uint32_t st = n % kStages;
+      if (!wait_all(p, sm, &sm.raw[st], (raw >> st) & 1u)) return;
+      raw ^= 1u << st;
+      const uint32_t v = smem_u32(sm.ring + st * 2 * kBlockBytes + kBlockBytes);
+#pragma unroll 1
+      for (int r = lane; r < 128; r += 32) {
+        const int c = 2 * blk + (r >> 6);
+        if (c < pc.ch.total && seen_by_some(pc.runs, pc.ch.key(c) + (r & 63))) continue;
+        for (int i = 0; i < 8; ++i) st_shared16(v + r * kRowBytes + i * 16, 0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.full[st]);
+    }
+    feed.done(sm, lane);
+  }
+}
+
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  float a, b;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(a), "=f"(b) : "r"(h));
-  return pack_bf16x2(a * scale, b * scale);
+  return h;
 }
-__device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// 8-bit caches: the codes go to a ring of raw blocks first, kRaw - 1 blocks ahead; each thread converts the
-// 16-byte pieces that it copied itself, so that waiting for its own copies is enough.
-__device__ __forceinline__ void loader_e4m3(const KvAttnParams& p, AttnSmem& sm, int warp, int lane) {
-  const int c = lane & 3, rr = lane >> 2;
+// 8-bit, warp 0: every block's TMA boxes of codes into the ring of raw blocks, and its scales.
+__device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
+  constexpr int kStages = Ring<true>::kStages, kRaw = Ring<true>::kRaw;
   const KvView& kv = p.kv;
   Walk w(p, sm.plan);
   Piece pc;
   uint32_t n = 0, pieces = 0;
   bool ok = true;
   while (ok && w.next(p, pc)) {
-    const int buf = pieces & 1;
-    if (pieces >= 2 && !wait_all(p, sm, &sm.q_empty[buf], ((pieces >> 1) - 1) & 1)) break;
-    ++pieces;
-    load_q(p, sm, pc, buf, warp, lane);
-    float ks[kRaw], vs[kRaw];  // lane g < 8: the scales of group g, of the blocks in flight
-    auto copy = [&](int blk, uint32_t slot, float& sk, float& sv) {
-      sk = sv = 1.f;
-      if (blk < pc.blk1) {
-        const int j = lane < 8 ? group_key(pc, blk, lane) : -1;
-        const int base = j >= 0 ? group_row(p, pc, j) : -1;
-        if (base >= 0) {
-          sk = kv.k_scale[base >> kv.page_log2];
-          sv = kv.v_scale[base >> kv.page_log2];
-        }
-        const int key0 = pc.ch.key(2 * blk), key1 = 2 * blk + 1 < pc.ch.total ? pc.ch.key(2 * blk + 1) : INT_MAX - 64;
-        const uint32_t dst = smem_u32(sm.raw[slot]) + lane * 16;
-#pragma unroll 2
-        for (int u = warp; u < 16; u += kLoaders) {  // eight rows of K and of V
-          const int r = 8 * u + rr;
-          const int row = __shfl_sync(0xffffffffu, base, u >> 1);
-          const bool have = row >= 0 && seen_by_some(pc.runs, (r < 64 ? key0 : key1 - 64) + r);
-          const long long at = have ? static_cast<long long>(row + (r & 15)) * kD + 16 * c : 0;
-          cp_async16(dst + u * 512, kv.k + at, have ? 16u : 0u);
-          cp_async16(dst + u * 512 + 8192, kv.v + at, have ? 16u : 0u);
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i + 1 < kRaw; ++i) copy(pc.blk0 + i, (n + i) % kRaw, ks[i], vs[i]);
+    if (!publish(p, sm, pieces, pc, lane)) {
+      ok = false;
+      break;
+    }
+    int lo = 200, hi = -200;  // exponents of the value scales
+    // page entries are loaded two blocks ahead, scales one
+    int row = box_row(p, pc, pc.blk0, lane, box_entry(p, pc, pc.blk0, lane));
+    int entry = box_entry(p, pc, pc.blk0 + 1, lane);
+    float sk = 1.f, sv = 1.f;
+    if (row >= 0) {
+      sk = kv.k_scale[row >> kv.page_log2];
+      sv = kv.v_scale[row >> kv.page_log2];
+    }
     for (int blk = pc.blk0; blk < pc.blk1; ++blk, ++n) {
-      copy(blk + kRaw - 1, (n + kRaw - 1) % kRaw, ks[kRaw - 1], vs[kRaw - 1]);
-      const uint32_t st = n % kStages;
-      if (n >= kStages && !wait_all(p, sm, &sm.empty[st], ((n / kStages) & 1) ^ 1)) {
+      const int next = box_row(p, pc, blk + 1, lane, entry);
+      entry = box_entry(p, pc, blk + 2, lane);
+      float nk = 1.f, nv = 1.f;
+      if (next >= 0) {
+        nk = kv.k_scale[next >> kv.page_log2];
+        nv = kv.v_scale[next >> kv.page_log2];
+      }
+      const uint32_t slot = n % kRaw;
+      if (n >= kRaw && !wait_all(p, sm, &sm.raw_empty[slot], ((n / kRaw) & 1) ^ 1)) {
         ok = false;
         break;
       }
-      cp_async_wait<kRaw - 1>();
-      const uint32_t src = smem_u32(sm.raw[n % kRaw]) + lane * 16, kd = smem_u32(sm.kv[st]);
+      const int e = static_cast<int>((__float_as_uint(sv) >> 23) & 0xffu) - 127;
+      if (lane < (128 >> p.box_log2)) {
+        lo = min(lo, e);
+        hi = max(hi, e);
+      }
+      const int g = lane & 7, box = (16 * g) >> p.box_log2;
+      const float k = __shfl_sync(0xffffffffu, sk, box);
+      const int lv = __shfl_sync(0xffffffffu, e, box);
+      if (lane < 8) {
+        ChunkScale& sc = sm.scale[n % kScales][g >> 2];
+        sc.k[g & 3] = k;
+        sc.lv[g & 3] = static_cast<float>(lv);
+        sc.vi[g & 3] = __uint_as_float(static_cast<uint32_t>(127 - lv) << 23);
+      }
+      if (blk + 1 == pc.blk1) {
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) sm.wild[pieces % kPieces] = hi - lo > kWild;
+      }
+      __syncwarp();
+      issue_boxes(p, mk, mv, pc, row, sm.ring + kStages * 2 * kBlockBytes + slot * kBlockBytes, &sm.raw[slot], kD, lane);
+      row = next;
+      sk = nk;
+      sv = nv;
+    }
+    ++pieces;
+  }
+  pc.blk1 = -1;
+  if (ok) publish(p, sm, pieces, pc, lane);
+  for (uint32_t c = n > kRaw ? n - kRaw : 0; c < n; ++c) mbar_wait_drain(&sm.raw[c % kRaw], (c / kRaw) & 1, kDrainBudget);
+}
+
+// 8-bit, warps 4 to 7: the raw codes to fp16 rows of the stage, eight rows of 64 codes at a time.
+__device__ __forceinline__ void convert_role(const KvAttnParams& p, AttnSmem& sm, int warp, int lane) {
+  constexpr int kStages = Ring<true>::kStages, kRaw = Ring<true>::kRaw;
+  const int c = lane & 3, rr = lane >> 2;
+  const uint32_t at0 = rr * kRowBytes + (((2 * c) ^ rr) << 4), at1 = rr * kRowBytes + (((2 * c + 1) ^ rr) << 4);
+  Feed feed;
+  uint32_t n = 0;
+  while (const Piece* next = feed.next(p, sm)) {
+    const int blk0 = next->blk0, blk1 = next->blk1;
+    for (int blk = blk0; blk < blk1; ++blk, ++n) {
+      const uint32_t st = n % kStages, slot = n % kRaw;
+      const bool whole = whole_block(*next, blk);
+      if (!wait_all(p, sm, &sm.raw[slot], (n / kRaw) & 1)) return;
+      if (n >= kStages && !wait_all(p, sm, &sm.empty[st], ((n / kStages) & 1) ^ 1)) return;
+      const uint8_t* src = sm.ring + kStages * 2 * kBlockBytes + slot * kBlockBytes + lane * 16;
+      uint8_t* dst = sm.ring + st * 2 * kBlockBytes;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half)
-#pragma unroll 2
-        for (int u = warp; u < 16; u += kLoaders) {
-          const float scale = __shfl_sync(0xffffffffu, half ? vs[0] : ks[0], u >> 1);
-          uint32_t x[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(src + u * 512 + half * 8192)
-                       : "memory");
-          const uint32_t row = kd + half * kBlockBytes + (8 * u + rr) * kRowBytes;  // row & 7 is rr
+      for (int u0 = warp; u0 < 32; u0 += 4 * kConverters) {  // K is units 0 to 15, V 16 to 31
+        uint4 x[4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            st_shared16(row + (((2 * c + i) ^ rr) << 4), bf16x2_of_e4m3(x[2 * i], scale),
-                        bf16x2_of_e4m3(x[2 * i] >> 16, scale), bf16x2_of_e4m3(x[2 * i + 1], scale),
-                        bf16x2_of_e4m3(x[2 * i + 1] >> 16, scale));
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (u0 + i * kConverters) * 512);
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * ((u0 + i * kConverters) & 15) + rr, ch = 2 * blk + (r >> 6);
+            if (ch >= next->ch.total || !seen_by_some(next->runs, next->ch.key(ch) + (r & 63))) x[i] = make_uint4(0, 0, 0, 0);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint8_t* to = dst + (u0 + i * kConverters) * 8 * kRowBytes;
+          *reinterpret_cast<uint4*>(to + at0) =
+              make_uint4(f16x2_of_e4m3(x[i].x), f16x2_of_e4m3(x[i].x >> 16), f16x2_of_e4m3(x[i].y), f16x2_of_e4m3(x[i].y >> 16));
+          *reinterpret_cast<uint4*>(to + at1) =
+              make_uint4(f16x2_of_e4m3(x[i].z), f16x2_of_e4m3(x[i].z >> 16), f16x2_of_e4m3(x[i].w), f16x2_of_e4m3(x[i].w >> 16));
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.full[st]);
-#pragma unroll
-      for (int i = 0; i + 1 < kRaw; ++i) {
-        ks[i] = ks[i + 1];
-        vs[i] = vs[i + 1];
+      if (lane == 0) {
+        mbar_arrive(&sm.raw_empty[slot]);
+        mbar_arrive(&sm.full[st]);
       }
     }
-    cp_async_wait<0>();
+    feed.done(sm, lane);
   }
-  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ products
 
 constexpr uint64_t kTileDesc = kBlockBytes >> 4, kStageDesc = 2 * kTileDesc;
 
-// S_t = Q_t K^T for one block of 128 keys
-__device__ __forceinline__ void issue_qk(uint64_t dq, uint64_t dk, uint32_t tmem, int t) {
-  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk) mma_ss(tmem + t * 256, dq + 2 * kk, dk + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+// kind::f16 with fp32 accumulators: bf16 operands, or fp16 ones
+template <bool kF16>
+__device__ constexpr uint32_t idesc_of(int n, int b_mn) {
+  return idesc_bf16_f32(128, n, 0, b_mn) & ~(kF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
-// Run by the whole warp (which keeps the descriptors uniform); one elected lane issues.  For each block and tile:
-// O += P V of each key half as soon as its warps have written P, then S = Q K^T of the next block, over P.
-__device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem) {
-  constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 64, 0, 1);
-  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
-  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.kv[0]), 16, 1024);
-  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.kv[0]) + kBlockBytes, 8192, 1024);
-  Walk w(p, sm.plan);
-  Piece pc;
-  uint32_t n = 0, pieces = 0;
-  uint32_t pfull[2] = {0, 0};
-  while (w.next(p, pc)) {
-    const int nblk = pc.blk1 - pc.blk0, tiles = pc.rows > 128 ? 2 : 1;
-    const uint64_t dq = q0 + (pieces & 1) * 2 * kTileDesc;
-    uint64_t* q_empty = &sm.q_empty[pieces & 1];
+// S of key half h: Q K^T for 64 keys
+template <bool kF16>
+__device__ __forceinline__ void issue_qk(uint64_t dq, uint64_t dk, uint32_t s_col) {
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) mma_ss(s_col, dq + 2 * kk, dk + 2 * kk, idesc_of<kF16>(64, 0), kk > 0 ? 1u : 0u);
+}
+
+// One warp for each tile; the whole warp runs (which keeps the descriptors uniform), one elected lane issues.  A key
+// half goes its own way: as soon as its warps have written P, its O += P V is issued and S = Q K^T of its next 64
+// keys behind it, over P.  One product of 128 keys for both halves would read Q from shared memory half as often
+// (tensor time 1024 cycles of a block of 256 rows against 1264), but ties the halves together.
+template <bool kF16>
+__device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem_base, int t, int lane) {
+  constexpr int kStages = Ring<kF16>::kStages;
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, tmem_base) + t * 256;
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024) + t * kTileDesc;
+  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.ring) + kBlockBytes, 8192, 1024);
+  Feed feed;
+  uint32_t n = 0, pieces = 0, pfull = 0;
+  while (const Piece* pc = feed.next(p, sm)) {
+    // a warp reduction's result is known to be uniform, so that counters and descriptors stay in uniform registers
+    const int nblk = __reduce_max_sync(0xffffffffu, pc->blk1 - pc->blk0);
+    const int rows = __reduce_max_sync(0xffffffffu, pc->rows);
+    feed.done(sm, lane);
+    const uint32_t buf = pieces & 1;
+    if (!wait_all(p, sm, &sm.q_full[buf], (pieces >> 1) & 1)) return;
     ++pieces;
-    {
-      const uint32_t st = n % kStages;
-      if (!wait_all(p, sm, &sm.full[st], (n / kStages) & 1)) return;
-      tc_fence_after();
-      if (elect_one()) {
-        for (int t = 0; t < tiles; ++t) {
-          issue_qk(dq + t * kTileDesc, k0 + st * kStageDesc, tmem, t);
-          mma_commit(&sm.s_full[t]);
-        }
-        if (nblk == 1) mma_commit(q_empty);
+    if (rows <= t * 128) {  // the item has one tile: this warp lets everything go
+      if (lane == 0) mbar_arrive(&sm.q_empty[buf]);
+      for (int j = 0; j < nblk; ++j, ++n) {
+        if (!wait_all(p, sm, &sm.full[n % kStages], (n / kStages) & 1)) return;
+        if (lane == 0) mbar_arrive(&sm.empty[n % kStages]);
       }
-      __syncwarp();
+      continue;
     }
-    for (int j = 0; j < nblk; ++j) {
-      const uint32_t cs = (n + j) % kStages;
+    const uint64_t dq = q0 + buf * 2 * kTileDesc;
+    if (!wait_all(p, sm, &sm.full[n % kStages], (n / kStages) & 1)) return;
+    tc_fence_after();
+    if (elect_one()) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        issue_qk<kF16>(dq, k0 + (n % kStages) * kStageDesc + h * (kTileDesc / 2), tmem + h * 64);
+        mma_commit(&sm.s_full[t][h]);
+      }
+      if (nblk == 1) mma_commit(&sm.q_empty[buf]);
+    }
+    __syncwarp();
+    for (int j = 0; j < nblk; ++j, ++n) {
+      const uint32_t cs = n % kStages, ns = (n + 1) % kStages;
       const bool more = j + 1 < nblk;
-      const uint32_t ns = (n + j + 1) % kStages;
-      if (more && !wait_all(p, sm, &sm.full[ns], ((n + j + 1) / kStages) & 1)) return;
-      tc_fence_after();
-      const uint64_t dv = v0 + cs * kStageDesc;
+      const uint64_t dv = v0 + cs * kStageDesc, dk = k0 + ns * kStageDesc;
+      if (more && !wait_all(p, sm, &sm.full[ns], ((n + 1) / kStages) & 1)) return;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t >= tiles) break;
-        const uint32_t s_col = tmem + t * 256, o_col = s_col + 128;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait_all(p, sm, &sm.p_full[t][h], pfull[t] & 1)) return;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(o_col + 64 * h, s_col + 64 * h + kk * 8, dv + 128 * (4 * h + kk), idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
-          }
-          __syncwarp();
-        }
-        ++pfull[t];
+      for (int h = 0; h < 2; ++h) {
+        if (!wait_all(p, sm, &sm.p_full[t][h], pfull & 1)) return;
+        tc_fence_after();
         if (elect_one()) {
+          const uint32_t s_col = tmem + h * 64, o_col = s_col + 128;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(o_col, s_col + kk * 8, dv + 128 * (4 * h + kk), idesc_of<kF16>(64, 1), j > 0 || kk > 0 ? 1u : 0u);
           if (more) {
-            issue_qk(dq + t * kTileDesc, k0 + ns * kStageDesc, tmem, t);
-            mma_commit(&sm.s_full[t]);
-          } else {
-            mma_commit(&sm.o_done[t]);
+            issue_qk<kF16>(dq, dk + h * (kTileDesc / 2), s_col);
+            mma_commit(&sm.s_full[t][h]);
+          }
+          if (h == 1) {
+            if (!more) mma_commit(&sm.o_done[t]);
+            mma_commit(&sm.empty[cs]);
+            if (j + 2 == nblk) mma_commit(&sm.q_empty[buf]);
           }
         }
         __syncwarp();
       }
-      if (elect_one()) {
-        mma_commit(&sm.empty[cs]);
-        if (j + 2 == nblk) mma_commit(q_empty);
-      }
-      __syncwarp();
+      ++pfull;
     }
-    n += nblk;
   }
 }
 
@@ -609,24 +738,191 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
   }
 }
 
+// Raises the rows' references to the largest logit of the chunk at least, and scales what was summed so far.  Returns
+// whether some row still has none (it has seen no key yet).
+template <bool kF16>
+__device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool first, uint64_t valid, float qs, const ChunkScale* sc,
+                                              float& m, float& l) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t s[16];
+    tmem_ld16(tS + 16 * c, s);
+    tmem_wait_ld();
+    float g = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      if ((valid >> (16 * c + q)) & 1ull) g = fmaxf(g, __uint_as_float(s[q]));
+    mx = fmaxf(mx, kF16 ? fmaf(g, qs * sc->k[c], sc->lv[c]) : g * kScaleLog2);
+  }
+  const float now = fmaxf(m, mx - (kF16 ? kF16Head : 0.f));
+  const float alpha = now == m ? 1.f : fast_exp2(m - now);  // m may be -inf: alpha = 0
+  m = now;
+  l *= alpha;
+  if (!first) rescale_o(tO, alpha);
+  return __any_sync(0xffffffffu, now == -INFINITY);
+}
+
+// 16 logits against the reference: weights as bf16 pairs, and their sums into rp.
+template <bool kF16, uint32_t kPoly, bool kMask>
+__device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t valid, float scale, float add, uint32_t* pk, float (&rp)[4]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float x0 = __uint_as_float(s[2 * q]), x1 = __uint_as_float(s[2 * q + 1]);
+    ffma2(x0, x1, scale, add);
+    if ((kPoly >> q) & 1u) {
+      exp2_poly2(x0, x1, x0, x1);
+    } else {
+      x0 = fast_exp2(x0);
+      x1 = fast_exp2(x1);
+    }
+    if (kMask) {
+      x0 = (valid >> (2 * q)) & 1u ? x0 : 0.f;
+      x1 = (valid >> (2 * q + 1)) & 1u ? x1 : 0.f;
+    }
+    fadd2(rp[2 * (q & 1)], rp[2 * (q & 1) + 1], x0, x1);
+    pk[q] = kF16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+  }
+}
+
+// A row's 64 logits, 16 at a time, the next 16 on their way.  Returns the sum of the weights as they enter P; `l` gets
+// that of the softmax's weights (8-bit: P holds the value scale too).
+template <bool kF16, bool kMask>
+__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, const ChunkScale* sc, uint32_t (&pk)[32],
+                                         float& l) {
+  const float ref = m == -INFINITY ? 0.f : m;
+  constexpr uint32_t kPoly = kMask ? 0u : kPolyPairs;
+  const uint32_t lo = static_cast<uint32_t>(valid), hi = static_cast<uint32_t>(valid >> 32);
+  uint32_t a[16], b[16];
+  tmem_ld16(tS, a);
+  if (kF16) {
+    const float4 k4 = *reinterpret_cast<const float4*>(sc->k), lv4 = *reinterpret_cast<const float4*>(sc->lv);
+    const float4 vi4 = *reinterpret_cast<const float4*>(sc->vi);
+    const float k[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs}, add[4] = {lv4.x - ref, lv4.y - ref, lv4.z - ref, lv4.w - ref};
+    const float vi[4] = {vi4.x, vi4.y, vi4.z, vi4.w};
+    tmem_wait_ld();
+    tmem_ld16(tS + 16, b);
+    float sum = 0.f;
+    l = 0.f;
+    auto group = [&](int c, const uint32_t(&s)[16], uint32_t v) {
+      float rp[4] = {0.f, 0.f, 0.f, 0.f};
+      weights16<true, kPoly & 0xffu, kMask>(s, v, k[c], add[c], pk + 8 * c, rp);
+      const float g = (rp[0] + rp[1]) + (rp[2] + rp[3]);
+      sum += g;
+      l = fmaf(g, vi[c], l);
+    };
+    group(0, a, lo);
+    tmem_wait_ld();
+    tmem_ld16(tS + 32, a);
+    group(1, b, lo >> 16);
+    tmem_wait_ld();
+    tmem_ld16(tS + 48, b);
+    group(2, a, hi);
+    tmem_wait_ld();
+    group(3, b, hi >> 16);
+    return sum;
+  }
+  tmem_wait_ld();
+  tmem_ld16(tS + 16, b);
+  float rp[4] = {0.f, 0.f, 0.f, 0.f};
+  weights16<false, (kPoly & 0xffu), kMask>(a, lo, kScaleLog2, -ref, pk, rp);
+  tmem_wait_ld();
+  tmem_ld16(tS + 32, a);
+  weights16<false, ((kPoly >> 8) & 0xffu), kMask>(b, lo >> 16, kScaleLog2, -ref, pk + 8, rp);
+  tmem_wait_ld();
+  tmem_ld16(tS + 48, b);
+  weights16<false, ((kPoly >> 16) & 0xffu), kMask>(a, hi, kScaleLog2, -ref, pk + 16, rp);
+  tmem_wait_ld();
+  weights16<false, (kPoly >> 24), kMask>(b, hi >> 16, kScaleLog2, -ref, pk + 24, rp);
+  l = (rp[0] + rp[1]) + (rp[2] + rp[3]);
+  return l;
+}
+
+// Half h of query row t * 128 + r of piece number i (by its softmax thread; the whole warp runs).  8-bit: as fp16 times a
+// power of two of the row (the row's largest has exponent 0; values below 2^-14 of it lose bits, 2^-25 of it at most).
+template <bool kF16>
+__device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, const Piece& pc, uint32_t i, int t, int h, int r, int lane) {
+  const uint32_t buf = i & 1;
+  if (i >= 2 && !wait_all(p, sm, &sm.q_empty[buf], ((i >> 1) - 1) & 1)) return false;
+  const int row = t * 128 + r;
+  if (pc.rows > t * 128) {
+    uint4 x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = make_uint4(0, 0, 0, 0);
+    uint32_t mx = 0;
+    if (row < pc.rows) {
+      const int a = pc.row0 + row, tok = a / p.group, head = pc.hk * p.group + a - tok * p.group;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (pc.s.row0 + tok) * p.q_ts + head * p.q_hs);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = src[4 * h + c];
+      if (kF16) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 y = c < 4 ? x[c] : src[4 * (h ^ 1) + c - 4];
+          const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx = max(mx, max((v[j] >> 7) & 0xffu, (v[j] >> 23) & 0xffu));
+        }
+      }
+    }
+    const int e = mx == 0xff ? 0 : min(max(static_cast<int>(mx) - 127, -120), 120);  // an infinity or NaN stays one
+    const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const uint32_t at = smem_u32(sm.q[buf][t]) + r * kRowBytes;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+      if (kF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
+      }
+      st_shared16(at + (((4 * h + c) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+    }
+    if (kF16) sm.q_scale[i % kPieces][row][h] = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    fence_proxy_async_smem();
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm.q_full[buf]);
+  return true;
+}
+
+template <bool kF16>
 __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem, int sw, int lane) {
   const int t = sw >> 3, h = (sw >> 2) & 1, wq = sw & 3;
   const int r = wq * 32 + lane;  // row of the tile
   const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
   const uint32_t tS = tmem + lane_off + t * 256 + h * 64, tO = tmem + lane_off + t * 256 + 128;
   bool withhold = p.withhold != 0 && blockIdx.x == 0 && sw == 0;  // test hook
-  Walk w(p, sm.plan);
-  Piece pc;
-  uint32_t sfull = 0, pieces = 0;
-  while (w.next(p, pc)) {
-    if (pc.rows <= t * 128) continue;  // the item has one tile
+  Feed feed;
+  uint32_t sfull = 0, pieces = 0, n = 0;  // pieces of this tile, key blocks of all
+  const Piece* next = feed.next(p, sm);
+  if (next && !load_query<kF16>(p, sm, *next, 0, t, h, r, lane)) return;
+  while (next) {
+    const Piece& pc = *next;
+    const uint32_t slot = feed.i % kPieces;
+    // the next piece's queries, before this one's end
+    auto look_ahead = [&]() {
+      Feed f = feed;
+      ++f.i;
+      next = f.next(p, sm);
+      return !next || load_query<kF16>(p, sm, *next, f.i, t, h, r, lane);
+    };
+    if (pc.rows <= t * 128) {  // the item has one tile
+      n += pc.blk1 - pc.blk0;
+      if (!look_ahead()) return;
+      feed.done(sm, lane);
+      continue;
+    }
     const int a = pc.row0 + min(t * 128 + r, pc.rows - 1), tok = a / p.group;
     const Span sp = span_of(p.win, pc.s.len - pc.s.n_new + tok, pc.s.len);
     float m = -INFINITY, l = 0.f;
+    bool unset = false;  // some row of the warp has no reference yet
     bool part = false;  // some streamed key is out of this row's sight
-    for (int blk = pc.blk0; blk < pc.blk1; ++blk) {
-      const int i = 2 * blk + h, j0 = pc.ch.key(i);
-      const bool have = i < pc.ch.total;
+    const Chunks ch = pc.ch;
+    const int blk0 = pc.blk0, blk1 = pc.blk1;
+    const float qs = kF16 ? sm.q_scale[slot][t * 128 + r][h] : kScaleLog2;
+    for (int blk = blk0; blk < blk1; ++blk, ++n) {
+      const int i = 2 * blk + h, j0 = ch.key(i);
+      const bool have = i < ch.total;
       const bool whole = have && ((j0 >= sp.lo && j0 + 64 <= sp.hi) || j0 + 64 <= sp.sink);
       const bool all = __all_sync(0xffffffffu, whole);
       uint64_t valid = ~0ull;
@@ -634,7 +930,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
         valid = have ? range_bits(sp.lo - j0, sp.hi - j0) | range_bits(0, sp.sink - j0) : 0ull;
         part |= have && !whole;
       }
-      if (!wait_all(p, sm, &sm.s_full[t], sfull & 1)) return;
+      if (!wait_all(p, sm, &sm.s_full[t][h], sfull & 1)) return;
       ++sfull;
       tc_fence_after();
       uint32_t pk[32];
@@ -642,53 +938,20 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
         // no row of this warp sees a key of the chunk
 #pragma unroll
         for (int q = 0; q < 32; ++q) pk[q] = 0u;
+        unset |= blk == blk0;
       } else {
-        float s[64];
-        {
-          uint32_t raw[64];
-          tmem_ld64(tS, raw);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(raw[q]);
+        const bool first = blk == blk0;
+        bool raise = first || unset;
+        const ChunkScale* sc = &sm.scale[n % kScales][h];
+        float part_l;
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          if (raise) unset = new_reference<kF16>(tS, tO + h * 64, first, valid, qs, sc, m, l);
+          const float sum = all ? weights<kF16, false>(tS, valid, m, qs, sc, pk, part_l) : weights<kF16, true>(tS, valid, m, qs, sc, pk, part_l);
+          raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)));  // far above the reference, or not a number
+          if (!raise || pass == 1) break;
         }
-        if (!all) {
-#pragma unroll
-          for (int q = 0; q < 64; ++q)
-            if (!((valid >> q) & 1ull)) s[q] = -INFINITY;
-        }
-        float mp[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mp[q] = s[q];
-#pragma unroll
-        for (int q = 2; q < 32; ++q) mp[q & 3] = max3f(mp[q & 3], s[2 * q], s[2 * q + 1]);
-        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * kScaleLog2;
-        if (blk == pc.blk0) {
-          m = mx;
-        } else {
-          const bool grow = mx > m + kGrow;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? fast_exp2(m - mx) : 1.f;  // m may be -inf: alpha = 0
-            rescale_o(tO + h * 64, alpha);
-            l *= alpha;
-            if (grow) m = mx;
-          }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        float rp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          float x0 = s[2 * q], x1 = s[2 * q + 1];
-          ffma2(x0, x1, kScaleLog2, -ref);
-          if ((kPolyPairs >> q) & 1u) {
-            exp2_poly2(x0, x1, x0, x1);
-          } else {
-            x0 = fast_exp2(x0);
-            x1 = fast_exp2(x1);
-          }
-          fadd2(rp[2 * (q & 1)], rp[2 * (q & 1) + 1], x0, x1);
-          pk[q] = pack_bf16x2(x0, x1);
-        }
-        l += (rp[0] + rp[1]) + (rp[2] + rp[3]);
+        l += part_l;
       }
       tmem_st32(tS, pk);
       tmem_wait_st();
@@ -699,6 +962,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       else if (lane == 0)
         mbar_arrive(&sm.p_full[t][h]);
     }
+    if (!look_ahead()) return;
     // join the two key halves; this thread finishes columns 32h..32h+31 of its row
     const uint32_t par = pieces & 1;
     ++pieces;
@@ -712,6 +976,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     const float* other = sm.stats[par][t][h ^ 1][r];
     const float mo = other[0], lo = fabsf(other[1]);
     part |= other[1] < 0.f;
+    const bool wild = kF16 && sm.wild[slot] != 0;
     const float mm = fmaxf(m, mo);
     const float fm = m == -INFINITY ? 0.f : fast_exp2(m - mm), fo = mo == -INFINITY ? 0.f : fast_exp2(mo - mm);
     const float den = l * fm + lo * fo;
@@ -736,8 +1001,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       if (h == 0) {
         sl.m[row] = mm;
         sl.l[row] = den;
-        sl.part[row] = part;
+        sl.part[row] = (part ? 1 : 0) | (wild ? 2 : 0);
       }
+      feed.done(sm, lane);
       continue;
     }
     const int head = pc.hk * p.group + a - tok * p.group;
@@ -745,7 +1011,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     bool bad = false;
 #pragma unroll
     for (int q = 0; q < 32; ++q) bad |= !(fabsf(o[q]) <= 3.402823466e+38f);
-    bad &= part;
+    bad = (bad && part) || wild;
     if (live && !bad) {
       const long long at = (pc.s.row0 + tok) * p.out_ts + head * p.out_hs + 32 * h;
       if (p.out_fp32) {
@@ -768,31 +1034,43 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       const int tk = __shfl_sync(0xffffffffu, tok, src), hd = __shfl_sync(0xffffffffu, head, src);
       exact_row(p, pc.b, pc.s.len, pc.s.row0 + tk, pc.s.len - pc.s.n_new + tk, hd, lane, 32 * h, 32 * h + 32);
     }
+    feed.done(sm, lane);
   }
 }
 
 template <bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
+    kv_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v) {
   extern __shared__ uint8_t smem_raw[];
   AttnSmem& sm = *reinterpret_cast<AttnSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], kLoaders);
-      mbar_init(&sm.empty[s], 1);
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&sm.full[s], kE4m3 ? kConverters : 2);
+      mbar_init(&sm.empty[s], 2);
+      mbar_init(&sm.raw[s], 1);
+      mbar_init(&sm.raw_empty[s], kConverters);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sm.q_empty[t], 1);
-      mbar_init(&sm.s_full[t], 1);
+      for (int i = 0; i < kPieces / 2; ++i) {
+        mbar_init(&sm.piece_full[2 * i + t], 1);
+        mbar_init(&sm.piece_empty[2 * i + t], Ring<kE4m3>::kWarps - (kE4m3 ? 2 : 1));
+      }
+      mbar_init(&sm.q_full[t], 16);
+      mbar_init(&sm.q_empty[t], 2);
+      mbar_init(&sm.drain[t], 1);
       mbar_init(&sm.o_done[t], 1);
-      for (int h = 0; h < 2; ++h) mbar_init(&sm.p_full[t][h], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.s_full[t][h], 1);
+        mbar_init(&sm.p_full[t][h], 4);
+      }
       for (int w = 0; w < 4; ++w) mbar_init(&sm.pair[t][w], 64);
     }
-    mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
   }
-  make_plan(p, sm.plan, reinterpret_cast<long long*>(sm.kv[0]));  // the ring is not in use yet
+  make_plan(p, sm.plan, reinterpret_cast<long long*>(sm.ring));  // the ring is not in use yet
   if (warp == 3) {
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
@@ -802,23 +1080,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  // registers: launched with 96 x 640; 64 x 128 + 104 x 512 are as many
-  if (warp < 4) {
-    reg_dealloc_dec<64>();
-    if (warp == 3) {
-      mma_role(p, sm, tmem);
+  // registers: launched with 96 x 640 or 80 x 768; 64 x 128 + 104 x 512 and 48 x 256 + 96 x 512 are as many
+  if (warp < Ring<kE4m3>::kSoftmax) {
+    if (kE4m3)
+      reg_dealloc_dec<48>();
+    else
+      reg_dealloc_dec<64>();
+    if (kE4m3 && warp >= 4) {
+      convert_role(p, sm, warp - 4, lane);
+    } else if (warp >= 2) {
+      mma_role<kE4m3>(p, sm, tmem, warp - 2, lane);
       // also after a wait that gave up: no product is in flight when the block lets its memory go
-      if (elect_one()) mma_commit(&sm.drain);
+      if (elect_one()) mma_commit(&sm.drain[warp - 2]);
       __syncwarp();
-      mbar_wait_drain(&sm.drain, 0, kDrainBudget);
-    } else if (kE4m3) {
-      loader_e4m3(p, sm, warp, lane);
-    } else {
-      loader_bf16(p, sm, warp, lane);
+      mbar_wait_drain(&sm.drain[warp - 2], 0, kDrainBudget);
+    } else if (kE4m3 && warp == 0) {
+      load_codes_role(p, sm, &map_k, &map_v, lane);
+    } else if (!kE4m3 && warp == 0) {
+      load_role(p, sm, &map_k, &map_v, lane);
+    } else if (!kE4m3) {
+      clear_role(p, sm, lane);
     }
   } else {
-    reg_alloc_inc<104>();
-    softmax_role(p, sm, tmem, warp - 4, lane);
+    if (kE4m3)
+      reg_alloc_inc<96>();
+    else
+      reg_alloc_inc<104>();
+    softmax_role<kE4m3>(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
   }
   __syncwarp();
   tc_fence_before();
@@ -837,7 +1125,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
   const int r = blockIdx.y * 32 + (threadIdx.x >> 3), col = (threadIdx.x & 7) * 8, lane = threadIdx.x & 31;
   if (!cut.valid || blockIdx.y * 32 >= cut.rows) return;
   float mm = -INFINITY, l = 0.f, o[8];
-  bool part = false;
+  bool part = false, wild = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
   int b0 = 0;
@@ -852,7 +1140,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
       o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g; o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
       o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g; o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
       l = l * f + sl.l[r] * g;
-      part |= sl.part[r] != 0;
+      part |= (sl.part[r] & 1) != 0;
+      wild |= (sl.part[r] & 2) != 0;
       mm = nm;
     }
     b0 = b1;
@@ -866,7 +1155,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
   }
   // a row is exact as a whole: its 8 threads agree
   const bool live = r < cut.rows;
-  uint32_t todo = __ballot_sync(0xffffffffu, live && bad && part);
+  uint32_t todo = __ballot_sync(0xffffffffu, live && ((bad && part) || wild));
   const bool mine = ((todo >> (lane & 24)) & 0xffu) != 0;
   const int a = cut.row0 + r, tok = a / p.group, head = cut.hk * p.group + a - tok * p.group;
   if (live && !mine) {
@@ -891,18 +1180,38 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
 
 size_t attn_workspace_bytes() { return sizeof(Work); }
 
-cudaError_t launch_attn(const KvAttnParams& p, cudaStream_t stream, int* n_launch) {
+saf3r_status launch_attn(const KvAttnParams& p0, cudaStream_t stream, int* n_launch) {
+  KvAttnParams p = p0;
+  const KvView& kv = p.kv;
+  CUtensorMap mk, mv;
+  bool ok;
+  if (p.ck) {
+    p.box_log2 = 6;
+    const long long head = static_cast<long long>(kv.n_tokens) * kD;
+    ok = make_map_rows(&mk, p.ck, kv.n_tokens, kD, kv.n_heads, head, 64) &&
+         make_map_rows(&mv, p.cv, kv.n_tokens, kD, kv.n_heads, head, 64);
+  } else {
+    p.box_log2 = kv.page_log2 < 6 ? kv.page_log2 : 6;
+    const int box = 1 << p.box_log2;
+    const long long rows = static_cast<long long>(kv.n_pages) * kv.n_heads * kv.page;
+    ok = p.e4m3 ? make_map_codes(&mk, kv.k, rows, box) && make_map_codes(&mv, kv.v, rows, box)
+                : make_map_rows(&mk, kv.k, rows, kD, 1, rows * kD, box) && make_map_rows(&mv, kv.v, rows, kD, 1, rows * kD, box);
+  }
+  if (!ok) return SAF3R_ERR_CUDA;
   const int smem = static_cast<int>(sizeof(AttnSmem) + 1024);
   const auto kernel = p.e4m3 ? kv_attn_kernel<true> : kv_attn_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess) return SAF3R_ERR_CUDA;
   const int grid = p.num_sms < kMaxShares ? p.num_sms : kMaxShares;
-  kernel<<<grid, kThreads, smem, stream>>>(p);
+  kernel<<<grid, 32 * (p.e4m3 ? Ring<true>::kWarps : Ring<false>::kWarps), smem, stream>>>(p, mk, mv);
   ++*n_launch;
-  if ((e = cudaGetLastError()) != cudaSuccess || grid == 1) return e;
-  kv_join_kernel<<<dim3(grid - 1, kItem / 32), 256, 0, stream>>>(p);
-  ++*n_launch;
-  return cudaGetLastError();
+  if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
+  if (grid > 1) {
+    kv_join_kernel<<<dim3(grid - 1, kItem / 32), 256, 0, stream>>>(p);
+    ++*n_launch;
+    if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
+  }
+  return SAF3R_OK;
 }
 
 }  // namespace saf3r

@@ -74,6 +74,7 @@ struct KvAttnParams {
   long long wait_budget;
   int32_t withhold;
   int32_t n_split;     // decode: most pieces of one item
+  int32_t box_log2;    // tensor cores: keys of one TMA box (a page, at most 64)
 };
 
 #ifdef __CUDACC__
@@ -158,7 +159,7 @@ cudaError_t launch_decode(const KvAttnParams& p, cudaStream_t stream, int* n_lau
 
 // the tensor-core kernel (kv_attn_sm100.cu)
 size_t attn_workspace_bytes();
-cudaError_t launch_attn(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
+saf3r_status launch_attn(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
 
 // host side of api.cu that the streaming entry points share
 bool call_device(int* sms, int* major, int** err);
@@ -168,5 +169,6 @@ long long call_wait_budget();
 bool take_withhold_arrive();
 bool make_map_rows(CUtensorMap* m, const void* base, long long rows, long long row_stride, int heads,
                    long long head_stride, int box_rows);
+bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows);
 
 }  // namespace saf3r

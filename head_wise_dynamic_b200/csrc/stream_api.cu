@@ -218,7 +218,7 @@ saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* ba
     st = cuda_status(launch_decode(p, static_cast<cudaStream_t>(stream), &launches));
   else {
     p.withhold = take_withhold_arrive();
-    st = cuda_status(launch_attn(p, static_cast<cudaStream_t>(stream), &launches));
+    st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
   }
   set_launch_count(launches);
   return st;
@@ -261,7 +261,7 @@ saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* w
   p.wait_budget = call_wait_budget();
   p.withhold = take_withhold_arrive();
   int launches = 0;
-  st = cuda_status(launch_attn(p, static_cast<cudaStream_t>(stream), &launches));
+  st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
   set_launch_count(launches);
   return st;
 }
