@@ -4,18 +4,18 @@
 // An item is 256 rows of one kv head (its group's heads times new tokens, token after token) of one sequence: two
 // 128-row tiles.  The keys that some row of the item sees (Runs) are streamed 128 at a time, as two
 // chunks of 64.  The items' key blocks, laid end to end, are cut into equal shares, one CTA each: an item
-// cut by a share's border is finished by the join kernel from its pieces' unnormalised sums.  Equal shares
+// cut by a share's border is finished by the join kernel from its pieces' answers.  Equal shares
 // keep every SM busy with few items (one view of one stream: 96 items of unequal length on 148 SMs).
 //
-// Warps (20):
+// Warps (20, or 24 with 8-bit caches):
 //   0-1    loaders: each block's K and V rows into a ring of stages, in the 128-byte-swizzled layout that the tensor
 //          core reads, a TMA box for each page (or 64 rows of it).  Value rows that no row of the item sees are cleared:
 //          what lies behind a sequence's end need not be finite.  bf16: TMA writes the stage itself.  8-bit: the
-//          codes land beside it and become fp16 (exact, one conversion for two).  The page's key scale multiplies the fp32
-//          logits; its value scale goes into the exponent, so that P is the weight times it; the row's sum takes
-//          it out again.
+//          codes land beside it, and four more warps (4-7) turn them into fp16 times their page's scale over the
+//          largest of the piece: exact where the scales are within 2^22 of one another, and the piece's rows go key by
+//          key where they are not.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
 //   2-3    issue the products, a warp for each tile.
-//   4-19   softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
+//   last 16 softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
 //          Sixteen warps, four for each scheduler in different steps, hide each other's waits.
 // Tensor memory (512 columns): for each tile S (128 fp32 columns; each half's P, bf16 or fp16, goes over the first 32
 // columns of its half once read) and an accumulator O for each key half (64 columns).  The halves have a
@@ -23,7 +23,7 @@
 //
 // Weights are 2^(x - reference), the reference a row's largest logit of its first block: bf16 P and the fp32 sums
 // keep their relative precision at any reference, so no maximum is taken of later blocks.  Only a block whose
-// weights sum to more than 2^24 moves it: its logits are read again, what was summed so far is scaled.
+// weights sum to more than 2^24 (fp16: 2^15) moves it: its logits are read again, what was summed so far is scaled.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -39,17 +39,17 @@ namespace saf3r {
 namespace {
 
 constexpr int kConverters = 4;         // warps that convert 8-bit codes
-constexpr int kScales = 8;             // blocks whose scales are kept: 3 raw ones and the 3 stages'
-constexpr int kMaxStages = 4;
+constexpr int kScales = 8;             // blocks whose scales are kept: 3 raw ones and the 4 stages'
+constexpr int kMaxStages = 5;
 constexpr int kPieces = 4;             // pieces that warp 0 may be ahead
 constexpr int kItem = 256;             // rows of an item
 constexpr int kRowBytes = 128;
 constexpr int kBlockBytes = 128 * kRowBytes;  // 128 rows x 64 bf16
 constexpr float kScaleLog2 = 0.18033688011112042f;  // log2(e) / sqrt(64)
 constexpr float kGrow = 16777216.f;    // a block's weights may sum to 2^24 before its rows' references move
-constexpr float kGrowF16 = 8192.f;     // fp16 P: within its range,
-constexpr float kF16Head = 6.f;        // and a first block's largest weight is 2^6, so that fp16 ends 2^-30 below it
-constexpr int kWild = 64;              // largest spread of value scales (in exponents) that P's fp32 sum is sure to bear
+constexpr float kGrowF16 = 32768.f;    // fp16 weights: 2^15
+constexpr int kCodeTop = 7;            // codes of a piece's largest scale are multiplied by 2^7 (448 * 2^7 is in fp16's range),
+constexpr int kWild = 22;              // those of scales down to 2^-22 of it by 2^-15 at least: exact in fp16, subnormal codes too
 constexpr int kMaxShares = 160;        // CTAs of a launch at most (one for each SM)
 constexpr int kPlanEntries = 1024;
 // Cost of a key block and of an item's start and end, in sixteenths of a two-tile block.
@@ -64,9 +64,9 @@ constexpr uint32_t kPolyPairs = POLY;
 // p(f) = 1 + f (c1 + f (c2 + f c3)), fitted to 2^f on [0, 1) for least maximum relative error (8.6e-5)
 constexpr float kExpC1 = 0.6951168179512024f, kExpC2 = 0.22764486074447632f, kExpC3 = 0.07706713676452637f;
 
-// A share's unfinished item: per row the sum of weights times values, their sum and reference maximum.
+// A share's part of an unfinished item: per row its answer, the sum of its weights and their reference.
 struct Slot {
-  float o[kItem][kD];
+  float o[kItem][kD];  // the piece's own answer: divided by l
   float m[kItem], l[kItem];
   int32_t part[kItem];  // nonzero: some streamed key is out of the row's sight
 };
@@ -135,22 +135,26 @@ struct Plan {
   int shares;
 };
 
-// Scales of a chunk's four groups of 16 keys: of the keys, log2 of the values' and one over the values'.
-struct alignas(16) ChunkScale {
-  float k[4], lv[4], vi[4];
+// 8-bit: what the codes of a block's groups of 16 keys are multiplied by, as pairs of fp16.
+struct alignas(16) BlockScale {
+  uint32_t k[8], v[8];
+};
+// 8-bit: exponents of the largest scales of a piece's keys and values, and whether some scale is too small beside them.
+struct PieceScale {
+  int k, v, wild;
 };
 
 // The ring of key blocks (stages of 128 rows of K, then of V) and, for 8-bit caches, the raw blocks behind it.
 template <bool kE4m3>
 struct Ring {
   static constexpr int kWarps = kE4m3 ? 24 : 20, kSoftmax = kWarps - 16;  // warps, the first softmax warp
-  static constexpr int kStages = kE4m3 ? 3 : 4, kRaw = kE4m3 ? 3 : 0;
+  static constexpr int kStages = kE4m3 ? 4 : 5, kRaw = kE4m3 ? 3 : 0;
   static constexpr int kBytes = (2 * kStages + kRaw) * kBlockBytes;
 };
 constexpr int kRingBytes = Ring<true>::kBytes > Ring<false>::kBytes ? Ring<true>::kBytes : Ring<false>::kBytes;
 
 struct AttnSmem {
-  uint8_t q[2][2][kBlockBytes];
+  uint8_t q[2][kBlockBytes];
   uint8_t ring[kRingBytes];
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t raw[kMaxStages], raw_empty[kMaxStages];
@@ -159,9 +163,10 @@ struct AttnSmem {
   uint64_t drain[2];
   uint64_t pair[2][4];                // the two warps of a tile's 32 rows meet here
   float stats[2][2][2][128][2];       // [piece parity][tile][half][row] = (reference, sum)
-  ChunkScale scale[kScales][2];       // 8-bit: scales of a block's chunks
-  float q_scale[kPieces][kItem][2];         // 8-bit: what a row's logits are multiplied by
-  int wild[kPieces];                  // 8-bit: the piece's value scales are too far apart for P
+  BlockScale scale[kScales];
+  PieceScale piece_scale[kPieces];
+  uint64_t scale_full[kPieces];
+  int16_t q_exp[kPieces][kItem][2];   // 8-bit: exponent of a row's queries, for each half's threads
   Plan plan;
   Piece pieces[kPieces];              // warp 0's walk, for the other warps; blk1 < 0: the end
   uint64_t piece_full[kPieces], piece_empty[kPieces];
@@ -494,7 +499,52 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// 8-bit, warp 0: every block's TMA boxes of codes into the ring of raw blocks, and its scales.
+__device__ __forceinline__ int exponent(float scale) { return static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu) - 127; }
+// 2^(kCodeTop + d) twice as fp16 (d <= 0; 0 below fp16's range)
+__device__ __forceinline__ uint32_t f16_power(int d) {
+  const int e = kCodeTop + d + 15;
+  const uint32_t h = e >= 1 && e < 31 ? static_cast<uint32_t>(e) << 10 : (e > -10 && e < 1 ? 1u << (e + 9) : 0u);
+  return h | (h << 16);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// 8-bit, warp 1: the largest scales of every piece.  A scale of 2^-100 is that of rows of zeros (or of values below 2^-91):
+// it does not count as too small.
+__device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, int lane) {
+  const KvView& kv = p.kv;
+  Feed feed;
+  while (const Piece* next = feed.next(p, sm)) {
+    const Piece& pc = *next;
+    int k_hi = -127, v_hi = -127, k_lo = 127, v_lo = 127;
+    const int per_log2 = 7 - p.box_log2;  // boxes of a block
+#pragma unroll 2
+    for (int i = (pc.blk0 << per_log2) + lane; i < (pc.blk1 << per_log2); i += 32) {
+      const int blk = i >> per_log2, box = i & ((1 << per_log2) - 1);
+      const int row = box_row(p, pc, blk, box, box_entry(p, pc, blk, box));
+      if (row < 0) continue;
+      const int k = exponent(kv.k_scale[row >> kv.page_log2]), v = exponent(kv.v_scale[row >> kv.page_log2]);
+      k_hi = max(k_hi, k);
+      v_hi = max(v_hi, v);
+      if (k > -100) k_lo = min(k_lo, k);
+      if (v > -100) v_lo = min(v_lo, v);
+    }
+    k_hi = __reduce_max_sync(0xffffffffu, k_hi);
+    v_hi = __reduce_max_sync(0xffffffffu, v_hi);
+    k_lo = __reduce_min_sync(0xffffffffu, k_lo);
+    v_lo = __reduce_min_sync(0xffffffffu, v_lo);
+    if (lane == 0) {
+      sm.piece_scale[feed.i % kPieces] = PieceScale{k_hi, v_hi, k_lo < k_hi - kWild || v_lo < v_hi - kWild};
+      mbar_arrive(&sm.scale_full[feed.i % kPieces]);
+    }
+    feed.done(sm, lane);
+  }
+}
+
+// 8-bit, warp 0: every block's TMA boxes of codes into the ring of raw blocks, and what they are multiplied by.
 __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
   constexpr int kStages = Ring<true>::kStages, kRaw = Ring<true>::kRaw;
   const KvView& kv = p.kv;
@@ -507,7 +557,6 @@ __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem&
       ok = false;
       break;
     }
-    int lo = 200, hi = -200;  // exponents of the value scales
     // page entries are loaded two blocks ahead, scales one
     int row = box_row(p, pc, pc.blk0, lane, box_entry(p, pc, pc.blk0, lane));
     int entry = box_entry(p, pc, pc.blk0 + 1, lane);
@@ -516,6 +565,8 @@ __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem&
       sk = kv.k_scale[row >> kv.page_log2];
       sv = kv.v_scale[row >> kv.page_log2];
     }
+    if (!wait_all(p, sm, &sm.scale_full[pieces % kPieces], (pieces / kPieces) & 1)) break;
+    const PieceScale top = sm.piece_scale[pieces % kPieces];
     for (int blk = pc.blk0; blk < pc.blk1; ++blk, ++n) {
       const int next = box_row(p, pc, blk + 1, lane, entry);
       entry = box_entry(p, pc, blk + 2, lane);
@@ -529,24 +580,11 @@ __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem&
         ok = false;
         break;
       }
-      const int e = static_cast<int>((__float_as_uint(sv) >> 23) & 0xffu) - 127;
-      if (lane < (128 >> p.box_log2)) {
-        lo = min(lo, e);
-        hi = max(hi, e);
-      }
       const int g = lane & 7, box = (16 * g) >> p.box_log2;
-      const float k = __shfl_sync(0xffffffffu, sk, box);
-      const int lv = __shfl_sync(0xffffffffu, e, box);
+      const float of = __shfl_sync(0xffffffffu, sk, box), ov = __shfl_sync(0xffffffffu, sv, box);
       if (lane < 8) {
-        ChunkScale& sc = sm.scale[n % kScales][g >> 2];
-        sc.k[g & 3] = k;
-        sc.lv[g & 3] = static_cast<float>(lv);
-        sc.vi[g & 3] = __uint_as_float(static_cast<uint32_t>(127 - lv) << 23);
-      }
-      if (blk + 1 == pc.blk1) {
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) sm.wild[pieces % kPieces] = hi - lo > kWild;
+        sm.scale[n % kScales].k[lane] = f16_power(exponent(of) - top.k);
+        sm.scale[n % kScales].v[lane] = f16_power(exponent(ov) - top.v);
       }
       __syncwarp();
       issue_boxes(p, mk, mv, pc, row, sm.ring + kStages * 2 * kBlockBytes + slot * kBlockBytes, &sm.raw[slot], kD, lane);
@@ -591,11 +629,18 @@ __device__ __forceinline__ void convert_role(const KvAttnParams& p, AttnSmem& sm
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint8_t* to = dst + (u0 + i * kConverters) * 8 * kRowBytes;
-          *reinterpret_cast<uint4*>(to + at0) =
-              make_uint4(f16x2_of_e4m3(x[i].x), f16x2_of_e4m3(x[i].x >> 16), f16x2_of_e4m3(x[i].y), f16x2_of_e4m3(x[i].y >> 16));
-          *reinterpret_cast<uint4*>(to + at1) =
-              make_uint4(f16x2_of_e4m3(x[i].z), f16x2_of_e4m3(x[i].z >> 16), f16x2_of_e4m3(x[i].w), f16x2_of_e4m3(x[i].w >> 16));
+          const int u = u0 + i * kConverters;
+          const uint32_t f = sm.scale[n % kScales].k[u >> 1];  // two units a group; v follows k
+          const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            h[2 * j] = mul_f16x2(f16x2_of_e4m3(y[j]), f);
+            h[2 * j + 1] = mul_f16x2(f16x2_of_e4m3(y[j] >> 16), f);
+          }
+          uint8_t* to = dst + u * 8 * kRowBytes;
+          *reinterpret_cast<uint4*>(to + at0) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(to + at1) = make_uint4(h[4], h[5], h[6], h[7]);
         }
       }
       fence_proxy_async_smem();
@@ -613,17 +658,17 @@ __device__ __forceinline__ void convert_role(const KvAttnParams& p, AttnSmem& sm
 
 constexpr uint64_t kTileDesc = kBlockBytes >> 4, kStageDesc = 2 * kTileDesc;
 
-// kind::f16 with fp32 accumulators: bf16 operands, or fp16 ones
+// M = 128, N = 64, fp32 accumulators; fp16 operands, or bf16 ones
 template <bool kF16>
-__device__ constexpr uint32_t idesc_of(int n, int b_mn) {
-  return idesc_bf16_f32(128, n, 0, b_mn) & ~(kF16 ? (1u << 7) | (1u << 10) : 0u);
+__device__ constexpr uint32_t idesc_of(int b_mn) {
+  return idesc_bf16_f32(128, 64, 0, b_mn) & ~(kF16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
 // S of key half h: Q K^T for 64 keys
 template <bool kF16>
 __device__ __forceinline__ void issue_qk(uint64_t dq, uint64_t dk, uint32_t s_col) {
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) mma_ss(s_col, dq + 2 * kk, dk + 2 * kk, idesc_of<kF16>(64, 0), kk > 0 ? 1u : 0u);
+  for (int kk = 0; kk < 4; ++kk) mma_ss(s_col, dq + 2 * kk, dk + 2 * kk, idesc_of<kF16>(0), kk > 0 ? 1u : 0u);
 }
 
 // One warp for each tile; the whole warp runs (which keeps the descriptors uniform), one elected lane issues.  A key
@@ -634,7 +679,7 @@ template <bool kF16>
 __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem_base, int t, int lane) {
   constexpr int kStages = Ring<kF16>::kStages;
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, tmem_base) + t * 256;
-  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024) + t * kTileDesc;
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[t]), 16, 1024);
   const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(smem_u32(sm.ring) + kBlockBytes, 8192, 1024);
   Feed feed;
@@ -644,27 +689,24 @@ __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, ui
     const int nblk = __reduce_max_sync(0xffffffffu, pc->blk1 - pc->blk0);
     const int rows = __reduce_max_sync(0xffffffffu, pc->rows);
     feed.done(sm, lane);
-    const uint32_t buf = pieces & 1;
-    if (!wait_all(p, sm, &sm.q_full[buf], (pieces >> 1) & 1)) return;
-    ++pieces;
     if (rows <= t * 128) {  // the item has one tile: this warp lets everything go
-      if (lane == 0) mbar_arrive(&sm.q_empty[buf]);
       for (int j = 0; j < nblk; ++j, ++n) {
         if (!wait_all(p, sm, &sm.full[n % kStages], (n / kStages) & 1)) return;
         if (lane == 0) mbar_arrive(&sm.empty[n % kStages]);
       }
       continue;
     }
-    const uint64_t dq = q0 + buf * 2 * kTileDesc;
+    if (!wait_all(p, sm, &sm.q_full[t], pieces & 1)) return;
+    ++pieces;
     if (!wait_all(p, sm, &sm.full[n % kStages], (n / kStages) & 1)) return;
     tc_fence_after();
     if (elect_one()) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        issue_qk<kF16>(dq, k0 + (n % kStages) * kStageDesc + h * (kTileDesc / 2), tmem + h * 64);
+        issue_qk<kF16>(q0, k0 + (n % kStages) * kStageDesc + h * (kTileDesc / 2), tmem + h * 64);
         mma_commit(&sm.s_full[t][h]);
       }
-      if (nblk == 1) mma_commit(&sm.q_empty[buf]);
+      if (nblk == 1) mma_commit(&sm.q_empty[t]);
     }
     __syncwarp();
     for (int j = 0; j < nblk; ++j, ++n) {
@@ -680,15 +722,15 @@ __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, ui
           const uint32_t s_col = tmem + h * 64, o_col = s_col + 128;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(o_col, s_col + kk * 8, dv + 128 * (4 * h + kk), idesc_of<kF16>(64, 1), j > 0 || kk > 0 ? 1u : 0u);
+            mma_ts(o_col, s_col + kk * 8, dv + 128 * (4 * h + kk), idesc_of<kF16>(1), j > 0 || kk > 0 ? 1u : 0u);
           if (more) {
-            issue_qk<kF16>(dq, dk + h * (kTileDesc / 2), s_col);
+            issue_qk<kF16>(q0, dk + h * (kTileDesc / 2), s_col);
             mma_commit(&sm.s_full[t][h]);
           }
           if (h == 1) {
             if (!more) mma_commit(&sm.o_done[t]);
             mma_commit(&sm.empty[cs]);
-            if (j + 2 == nblk) mma_commit(&sm.q_empty[buf]);
+            if (j + 2 == nblk) mma_commit(&sm.q_empty[t]);
           }
         }
         __syncwarp();
@@ -740,9 +782,8 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 
 // Raises the rows' references to the largest logit of the chunk at least, and scales what was summed so far.  Returns
 // whether some row still has none (it has seen no key yet).
-template <bool kF16>
-__device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool first, uint64_t valid, float qs, const ChunkScale* sc,
-                                              float& m, float& l) {
+__device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool first, uint64_t valid, float qs, float& m,
+                                              float& l) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -753,9 +794,9 @@ __device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool fir
 #pragma unroll
     for (int q = 0; q < 16; ++q)
       if ((valid >> (16 * c + q)) & 1ull) g = fmaxf(g, __uint_as_float(s[q]));
-    mx = fmaxf(mx, kF16 ? fmaf(g, qs * sc->k[c], sc->lv[c]) : g * kScaleLog2);
+    mx = fmaxf(mx, g * qs);
   }
-  const float now = fmaxf(m, mx - (kF16 ? kF16Head : 0.f));
+  const float now = fmaxf(m, mx);
   const float alpha = now == m ? 1.f : fast_exp2(m - now);  // m may be -inf: alpha = 0
   m = now;
   l *= alpha;
@@ -785,67 +826,39 @@ __device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t vali
   }
 }
 
-// A row's 64 logits, 16 at a time, the next 16 on their way.  Returns the sum of the weights as they enter P; `l` gets
-// that of the softmax's weights (8-bit: P holds the value scale too).
+// A row's 64 logits, 16 at a time, the next 16 on their way.
 template <bool kF16, bool kMask>
-__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, const ChunkScale* sc, uint32_t (&pk)[32],
-                                         float& l) {
-  const float ref = m == -INFINITY ? 0.f : m;
+__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, uint32_t (&pk)[32]) {
+  const float add = m == -INFINITY ? 0.f : -m;
   constexpr uint32_t kPoly = kMask ? 0u : kPolyPairs;
   const uint32_t lo = static_cast<uint32_t>(valid), hi = static_cast<uint32_t>(valid >> 32);
+  float rp[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t a[16], b[16];
   tmem_ld16(tS, a);
-  if (kF16) {
-    const float4 k4 = *reinterpret_cast<const float4*>(sc->k), lv4 = *reinterpret_cast<const float4*>(sc->lv);
-    const float4 vi4 = *reinterpret_cast<const float4*>(sc->vi);
-    const float k[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs}, add[4] = {lv4.x - ref, lv4.y - ref, lv4.z - ref, lv4.w - ref};
-    const float vi[4] = {vi4.x, vi4.y, vi4.z, vi4.w};
-    tmem_wait_ld();
-    tmem_ld16(tS + 16, b);
-    float sum = 0.f;
-    l = 0.f;
-    auto group = [&](int c, const uint32_t(&s)[16], uint32_t v) {
-      float rp[4] = {0.f, 0.f, 0.f, 0.f};
-      weights16<true, kPoly & 0xffu, kMask>(s, v, k[c], add[c], pk + 8 * c, rp);
-      const float g = (rp[0] + rp[1]) + (rp[2] + rp[3]);
-      sum += g;
-      l = fmaf(g, vi[c], l);
-    };
-    group(0, a, lo);
-    tmem_wait_ld();
-    tmem_ld16(tS + 32, a);
-    group(1, b, lo >> 16);
-    tmem_wait_ld();
-    tmem_ld16(tS + 48, b);
-    group(2, a, hi);
-    tmem_wait_ld();
-    group(3, b, hi >> 16);
-    return sum;
-  }
   tmem_wait_ld();
   tmem_ld16(tS + 16, b);
-  float rp[4] = {0.f, 0.f, 0.f, 0.f};
-  weights16<false, (kPoly & 0xffu), kMask>(a, lo, kScaleLog2, -ref, pk, rp);
+  weights16<kF16, (kPoly & 0xffu), kMask>(a, lo, qs, add, pk, rp);
   tmem_wait_ld();
   tmem_ld16(tS + 32, a);
-  weights16<false, ((kPoly >> 8) & 0xffu), kMask>(b, lo >> 16, kScaleLog2, -ref, pk + 8, rp);
+  weights16<kF16, ((kPoly >> 8) & 0xffu), kMask>(b, lo >> 16, qs, add, pk + 8, rp);
   tmem_wait_ld();
   tmem_ld16(tS + 48, b);
-  weights16<false, ((kPoly >> 16) & 0xffu), kMask>(a, hi, kScaleLog2, -ref, pk + 16, rp);
+  weights16<kF16, ((kPoly >> 16) & 0xffu), kMask>(a, hi, qs, add, pk + 16, rp);
   tmem_wait_ld();
-  weights16<false, (kPoly >> 24), kMask>(b, hi >> 16, kScaleLog2, -ref, pk + 24, rp);
-  l = (rp[0] + rp[1]) + (rp[2] + rp[3]);
-  return l;
+  weights16<kF16, (kPoly >> 24), kMask>(b, hi >> 16, qs, add, pk + 24, rp);
+  return (rp[0] + rp[1]) + (rp[2] + rp[3]);
 }
 
-// Half h of query row t * 128 + r of piece number i (by its softmax thread; the whole warp runs).  8-bit: as fp16 times a
-// power of two of the row (the row's largest has exponent 0; values below 2^-14 of it lose bits, 2^-25 of it at most).
+// Half h of query row t * 128 + r of a piece, the tile's number i (by its softmax thread; the whole warp runs).  8-bit: as
+// fp16 times a power of two of the row (the row's largest has exponent 0; values below 2^-14 of it lose bits, 2^-25 of it
+// at most).
 template <bool kF16>
-__device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, const Piece& pc, uint32_t i, int t, int h, int r, int lane) {
-  const uint32_t buf = i & 1;
-  if (i >= 2 && !wait_all(p, sm, &sm.q_empty[buf], ((i >> 1) - 1) & 1)) return false;
+__device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, const Piece& pc, uint32_t i, uint32_t slot, int t,
+                                           int h, int r, int lane) {
+  if (pc.rows <= t * 128) return true;
+  if (i >= 1 && !wait_all(p, sm, &sm.q_empty[t], (i & 1) ^ 1)) return false;
   const int row = t * 128 + r;
-  if (pc.rows > t * 128) {
+  {
     uint4 x[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) x[c] = make_uint4(0, 0, 0, 0);
@@ -867,7 +880,7 @@ __device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, 
     }
     const int e = mx == 0xff ? 0 : min(max(static_cast<int>(mx) - 127, -120), 120);  // an infinity or NaN stays one
     const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    const uint32_t at = smem_u32(sm.q[buf][t]) + r * kRowBytes;
+    const uint32_t at = smem_u32(sm.q[t]) + r * kRowBytes;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -877,11 +890,11 @@ __device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, 
       }
       st_shared16(at + (((4 * h + c) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
     }
-    if (kF16) sm.q_scale[i % kPieces][row][h] = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (kF16) sm.q_exp[slot][row][h] = static_cast<int16_t>(e);
     fence_proxy_async_smem();
   }
   __syncwarp();
-  if (lane == 0) mbar_arrive(&sm.q_full[buf]);
+  if (lane == 0) mbar_arrive(&sm.q_full[t]);
   return true;
 }
 
@@ -895,7 +908,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
   Feed feed;
   uint32_t sfull = 0, pieces = 0, n = 0;  // pieces of this tile, key blocks of all
   const Piece* next = feed.next(p, sm);
-  if (next && !load_query<kF16>(p, sm, *next, 0, t, h, r, lane)) return;
+  if (next && !load_query<kF16>(p, sm, *next, 0, 0, t, h, r, lane)) return;
   while (next) {
     const Piece& pc = *next;
     const uint32_t slot = feed.i % kPieces;
@@ -904,7 +917,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       Feed f = feed;
       ++f.i;
       next = f.next(p, sm);
-      return !next || load_query<kF16>(p, sm, *next, f.i, t, h, r, lane);
+      return !next || load_query<kF16>(p, sm, *next, pieces, f.i % kPieces, t, h, r, lane);
     };
     if (pc.rows <= t * 128) {  // the item has one tile
       n += pc.blk1 - pc.blk0;
@@ -919,7 +932,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     bool part = false;  // some streamed key is out of this row's sight
     const Chunks ch = pc.ch;
     const int blk0 = pc.blk0, blk1 = pc.blk1;
-    const float qs = kF16 ? sm.q_scale[slot][t * 128 + r][h] : kScaleLog2;
+    float qs = kScaleLog2;
     for (int blk = blk0; blk < blk1; ++blk, ++n) {
       const int i = 2 * blk + h, j0 = ch.key(i);
       const bool have = i < ch.total;
@@ -933,6 +946,10 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       if (!wait_all(p, sm, &sm.s_full[t][h], sfull & 1)) return;
       ++sfull;
       tc_fence_after();
+      if (kF16 && blk == blk0) {
+        const int e = sm.q_exp[slot][t * 128 + r][h] + sm.piece_scale[slot].k - kCodeTop;
+        qs = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + min(max(e, -126), 127)) << 23);
+      }
       uint32_t pk[32];
       if (!all && __all_sync(0xffffffffu, valid == 0ull)) {
         // no row of this warp sees a key of the chunk
@@ -942,16 +959,15 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       } else {
         const bool first = blk == blk0;
         bool raise = first || unset;
-        const ChunkScale* sc = &sm.scale[n % kScales][h];
-        float part_l;
+        float sum;
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
-          if (raise) unset = new_reference<kF16>(tS, tO + h * 64, first, valid, qs, sc, m, l);
-          const float sum = all ? weights<kF16, false>(tS, valid, m, qs, sc, pk, part_l) : weights<kF16, true>(tS, valid, m, qs, sc, pk, part_l);
+          if (raise) unset = new_reference(tS, tO + h * 64, first, valid, qs, m, l);
+          sum = all ? weights<kF16, false>(tS, valid, m, qs, pk) : weights<kF16, true>(tS, valid, m, qs, pk);
           raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)));  // far above the reference, or not a number
           if (!raise || pass == 1) break;
         }
-        l += part_l;
+        l += sum;
       }
       tmem_st32(tS, pk);
       tmem_wait_st();
@@ -962,10 +978,10 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       else if (lane == 0)
         mbar_arrive(&sm.p_full[t][h]);
     }
-    if (!look_ahead()) return;
-    // join the two key halves; this thread finishes columns 32h..32h+31 of its row
     const uint32_t par = pieces & 1;
     ++pieces;
+    if (!look_ahead()) return;
+    // join the two key halves; this thread finishes columns 32h..32h+31 of its row
     float* mine = sm.stats[par][t][h][r];
     mine[0] = m;
     mine[1] = part ? -l - 1e-30f : l;  // the sign says that some keys are out of sight
@@ -976,11 +992,12 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     const float* other = sm.stats[par][t][h ^ 1][r];
     const float mo = other[0], lo = fabsf(other[1]);
     part |= other[1] < 0.f;
-    const bool wild = kF16 && sm.wild[slot] != 0;
+    const bool wild = kF16 && sm.piece_scale[slot].wild != 0;
     const float mm = fmaxf(m, mo);
     const float fm = m == -INFINITY ? 0.f : fast_exp2(m - mm), fo = mo == -INFINITY ? 0.f : fast_exp2(mo - mm);
     const float den = l * fm + lo * fo;
-    const float scale = pc.slot >= 0 ? 1.f : (den == 0.f ? 0.f : 1.f / den);
+    float scale = den == 0.f ? 0.f : 1.f / den;
+    if (kF16) scale *= __uint_as_float(static_cast<uint32_t>(127 + max(sm.piece_scale[slot].v - kCodeTop, -126)) << 23);
     const float f0 = (h ? fo : fm) * scale, f1 = (h ? fm : fo) * scale;
     float o[32];
     {
@@ -1055,10 +1072,11 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
     for (int t = 0; t < 2; ++t) {
       for (int i = 0; i < kPieces / 2; ++i) {
         mbar_init(&sm.piece_full[2 * i + t], 1);
-        mbar_init(&sm.piece_empty[2 * i + t], Ring<kE4m3>::kWarps - (kE4m3 ? 2 : 1));
+        mbar_init(&sm.piece_empty[2 * i + t], Ring<kE4m3>::kWarps - 1);
+        mbar_init(&sm.scale_full[2 * i + t], 1);
       }
-      mbar_init(&sm.q_full[t], 16);
-      mbar_init(&sm.q_empty[t], 2);
+      mbar_init(&sm.q_full[t], 8);
+      mbar_init(&sm.q_empty[t], 1);
       mbar_init(&sm.drain[t], 1);
       mbar_init(&sm.o_done[t], 1);
       for (int h = 0; h < 2; ++h) {
@@ -1080,10 +1098,10 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  // registers: launched with 96 x 640 or 80 x 768; 64 x 128 + 104 x 512 and 48 x 256 + 96 x 512 are as many
+  // registers: launched with 96 x 640 or 80 x 768; 64 x 128 + 104 x 512 and 64 x 256 + 88 x 512 are as many
   if (warp < Ring<kE4m3>::kSoftmax) {
     if (kE4m3)
-      reg_dealloc_dec<48>();
+      reg_dealloc_dec<64>();
     else
       reg_dealloc_dec<64>();
     if (kE4m3 && warp >= 4) {
@@ -1098,12 +1116,14 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
       load_codes_role(p, sm, &map_k, &map_v, lane);
     } else if (!kE4m3 && warp == 0) {
       load_role(p, sm, &map_k, &map_v, lane);
-    } else if (!kE4m3) {
+    } else if (kE4m3) {
+      scan_role(p, sm, lane);
+    } else {
       clear_role(p, sm, lane);
     }
   } else {
     if (kE4m3)
-      reg_alloc_inc<96>();
+      reg_alloc_inc<88>();
     else
       reg_alloc_inc<104>();
     softmax_role<kE4m3>(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
@@ -1134,12 +1154,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     if (b1 > b0) {
       const Slot& sl = wk.slots[c][b0 > 0 ? 0 : 1];
       const float m = sl.m[r], nm = fmaxf(mm, m);
-      const float f = mm == -INFINITY ? 0.f : fast_exp2(mm - nm), g = m == -INFINITY ? 0.f : fast_exp2(m - nm);
+      const float f = mm == -INFINITY ? 0.f : fast_exp2(mm - nm), g = m == -INFINITY ? 0.f : fast_exp2(m - nm) * sl.l[r];
       const float4* src = reinterpret_cast<const float4*>(&sl.o[r][col]);
       const float4 x = src[0], y = src[1];
       o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g; o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
       o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g; o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
-      l = l * f + sl.l[r] * g;
+      l = l * f + g;
       part |= (sl.part[r] & 1) != 0;
       wild |= (sl.part[r] & 2) != 0;
       mm = nm;
