@@ -57,10 +57,7 @@ constexpr int kCost2 = 16, kCost1 = 13, kCostItem = 16;
 constexpr int kLeastShare = 4 * kCost2;  // shares smaller than this are not worth a CTA
 
 // Pairs (of the 32 of a row's 64 keys) whose exponentials run on the FMA pipe.
-#ifndef POLY
-#define POLY 0x88888888u
-#endif
-constexpr uint32_t kPolyPairs = POLY;
+constexpr uint32_t kPolyPairs = 0x80808080u;
 // p(f) = 1 + f (c1 + f (c2 + f c3)), fitted to 2^f on [0, 1) for least maximum relative error (8.6e-5)
 constexpr float kExpC1 = 0.6951168179512024f, kExpC2 = 0.22764486074447632f, kExpC3 = 0.07706713676452637f;
 
@@ -76,9 +73,9 @@ static_assert(sizeof(Slot) % 16 == 0, "slots stay aligned");
 struct Cut {
   int32_t valid, b, hk, row0, rows;
   int32_t first, n_new, len;  // the sequence
-  int32_t nblk, unit, shares;
+  int32_t nblk, unit, extra;
   int32_t pad;
-  long long x0, total;
+  long long x0, each;  // where the item begins; share_start's
 };
 
 struct Work {
@@ -107,8 +104,8 @@ __device__ __forceinline__ Tile tile_of(const KvAttnParams& p, const SeqInfo& s,
   const int r0 = i * kItem;
   t.rows = min(kItem, s.n_new * p.group - r0);
   const int start = s.len - s.n_new;
-  const Span a = span_of(p.win, start + r0 / p.group, s.len);
-  const Span z = span_of(p.win, start + (r0 + t.rows - 1) / p.group, s.len);
+  const Span a = span_of(p.win, start + p.by_group.div(r0), s.len);
+  const Span z = span_of(p.win, start + p.by_group.div(r0 + t.rows - 1), s.len);
   t.runs = runs_of(a.lo, z.hi, z.sink);
   t.ch = chunks_of(t.runs);
   t.nblk = (t.ch.total + 1) >> 1;
@@ -124,16 +121,12 @@ __device__ __forceinline__ int tiles_of(const KvAttnParams& p, const SeqInfo& s)
 // Blocks of an item that lie before distance d from its start.
 __device__ __forceinline__ int blocks_before(long long d, int nblk, int unit) {
   if (d <= 0) return 0;
-  const long long n = (d + unit - 1) / unit;
-  return n < nblk ? static_cast<int>(n) : nblk;
+  if (d >= static_cast<long long>(nblk) * unit) return nblk;
+  return (static_cast<int>(d) + unit - 1) / unit;
 }
 
-// This CTA's share: its range of the line of all items, and the item that holds its start.
-struct Plan {
-  long long xs, xe, x;  // range; start of the first item
-  int hk, b, tile;
-  int shares;
-};
+// Where share i of the line starts: the first `extra` shares have one unit more than `each`.
+__host__ __device__ __forceinline__ long long share_start(long long each, int extra, int i) { return each * i + (i < extra ? i : extra); }
 
 // 8-bit: what the codes of a block's groups of 16 keys are multiplied by, as pairs of fp16.
 struct alignas(16) BlockScale {
@@ -142,6 +135,62 @@ struct alignas(16) BlockScale {
 // 8-bit: exponents of the largest scales of a piece's keys and values, and whether some scale is too small beside them.
 struct PieceScale {
   int k, v, wild;
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// Cost of a sequence's tiles for one kv head (run by a warp).
+__device__ __forceinline__ long long seq_cost(const KvAttnParams& p, int b, int lane) {
+  const SeqInfo s = seq_info(p.kv, b);
+  const int n = tiles_of(p, s);
+  long long c = 0;
+  for (int i = lane; i < n; i += 32) c += tile_of(p, s, i).cost;
+  return warp_sum(c);
+}
+
+// Walks the pieces of this CTA's share: the range xs..xe of the line of all items (warp 0).
+struct Walk {
+  long long x, xs, xe;  // x: start of the item at (hk, b, tile)
+  int hk, b, tile;
+  SeqInfo s;
+
+  __device__ __forceinline__ bool next(const KvAttnParams& p, Piece& pc) {
+    while (x < xe) {
+      while (tile >= tiles_of(p, s)) {
+        tile = 0;
+        if (++b == p.kv.n_seqs) {
+          b = 0;
+          if (++hk == p.kv.n_heads) break;
+        }
+        s = seq_info(p.kv, b);
+      }
+      if (hk == p.kv.n_heads) break;
+      const Tile t = tile_of(p, s, tile);
+      const int b0 = blocks_before(xs - x, t.nblk, t.unit), b1 = blocks_before(xe - x, t.nblk, t.unit);
+      const int row0 = tile * kItem;
+      x += t.cost;
+      ++tile;
+      if (b0 < b1) {
+        pc.b = b;
+        pc.hk = hk;
+        pc.row0 = row0;
+        pc.rows = t.rows;
+        pc.s = s;
+        pc.runs = t.runs;
+        pc.ch = t.ch;
+        pc.blk0 = b0;
+        pc.blk1 = b1;
+        pc.slot = b0 > 0 ? 0 : (b1 < t.nblk ? 1 : -1);
+        return true;
+      }
+    }
+    pc.blk1 = -1;
+    return false;
+  }
 };
 
 // The ring of key blocks (stages of 128 rows of K, then of V) and, for 8-bit caches, the raw blocks behind it.
@@ -167,30 +216,26 @@ struct AttnSmem {
   PieceScale piece_scale[kPieces];
   uint64_t scale_full[kPieces];
   int16_t q_exp[kPieces][kItem][2];   // 8-bit: exponent of a row's queries, for each half's threads
-  Plan plan;
+  Walk walk;
   Piece pieces[kPieces];              // warp 0's walk, for the other warps; blk1 < 0: the end
   uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint32_t tmem_base;
   int abort;
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
+// Inclusive sums over a warp's lanes.
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
   return v;
 }
 
-// Cost of a sequence's tiles for one kv head (run by a warp).
-__device__ __forceinline__ long long seq_cost(const KvAttnParams& p, int b, int lane) {
-  const SeqInfo s = seq_info(p.kv, b);
-  const int n = tiles_of(p, s);
-  long long c = 0;
-  for (int i = lane; i < n; i += 32) c += tile_of(p, s, i).cost;
-  return warp_sum(c);
-}
-
-// Finds this CTA's share (run by all threads; `entries` is scratch in shared memory).
-__device__ void make_plan(const KvAttnParams& p, Plan& plan, long long* entries) {
+// Finds this CTA's share and its first piece (run by all threads; `entries` is scratch in shared memory).  Nothing is
+// planned ahead in a kernel of its own: the lengths are on the device, and a launch would cost more than this.
+__device__ __forceinline__ void make_plan(const KvAttnParams& p, Walk& walk, Piece& first, long long* entries) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.kv.n_seqs + kPlanEntries - 1) / kPlanEntries;
   const int n = (p.kv.n_seqs + per - 1) / per;
@@ -205,130 +250,77 @@ __device__ void make_plan(const KvAttnParams& p, Plan& plan, long long* entries)
   for (int e = lane; e < n; e += 32) mine += entries[e];
   const long long head = warp_sum(mine);  // of one kv head
   const long long total = head * p.kv.n_heads;
-  const long long most = total / kLeastShare;
-  const int shares = most < 1 ? 1 : (most < gridDim.x ? static_cast<int>(most) : gridDim.x);
+  const int shares = total >= static_cast<long long>(gridDim.x) * kLeastShare ? gridDim.x : max(1, static_cast<int>(total) / kLeastShare);
   const int me = blockIdx.x;
-  Plan pl;
-  pl.shares = shares;
-  pl.xs = total * me / shares;
-  pl.xe = me < shares ? total * (me + 1) / shares : pl.xs;
-  pl.x = pl.xs;
-  pl.hk = pl.b = pl.tile = 0;
+  const long long each = total / shares;
+  const int extra = static_cast<int>(total - each * shares);
+  Walk w;
+  w.xs = me < shares ? share_start(each, extra, me) : total;
+  w.xe = me < shares ? share_start(each, extra, me + 1) : total;
+  w.x = w.xs;
+  w.hk = w.b = w.tile = 0;
+  w.s = SeqInfo{0, 0, 0, false};
   Cut cut{};
-  if (pl.xs < pl.xe) {
-    pl.hk = static_cast<int>(pl.xs / head);
-    long long rest = pl.xs - pl.hk * head;  // inside the head
-    int e = 0;
-    for (int e0 = 0;; e0 += 32) {
-      const long long c = e0 + lane < n ? entries[e0 + lane] : 0;
-      long long incl = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
+  if (w.xs < w.xe) {
+    long long rest = w.xs;  // inside what is left
+    while (rest >= head) {
+      rest -= head;
+      ++w.hk;
+    }
+    for (int e0 = 0; e0 < n; e0 += 32) {
+      const long long c = e0 + lane < n ? entries[e0 + lane] : 0, incl = warp_scan(c, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, rest < incl);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        e = e0 + src;
+        w.b = (e0 + src) * per;
         rest -= __shfl_sync(0xffffffffu, incl - c, src);
         break;
       }
       rest -= __shfl_sync(0xffffffffu, incl, 31);
-      if (e0 + 32 >= n) break;  // not reached: rest < head
     }
-    int b = e * per;
-    for (; b + 1 < p.kv.n_seqs; ++b) {
-      const long long c = seq_cost(p, b, lane);
+    for (; per > 1 && w.b + 1 < p.kv.n_seqs; ++w.b) {
+      const long long c = seq_cost(p, w.b, lane);
       if (rest < c) break;
       rest -= c;
     }
-    const SeqInfo s = seq_info(p.kv, b);
-    const int nt = tiles_of(p, s);
+    w.s = seq_info(p.kv, w.b);
+    const int nt = tiles_of(p, w.s);
     for (int t0 = 0; t0 < nt; t0 += 32) {
-      const long long c = t0 + lane < nt ? tile_of(p, s, t0 + lane).cost : 0;
-      long long incl = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
+      const long long c = t0 + lane < nt ? tile_of(p, w.s, t0 + lane).cost : 0, incl = warp_scan(c, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, rest < incl);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        pl.tile = t0 + src;
+        w.tile = t0 + src;
         rest -= __shfl_sync(0xffffffffu, incl - c, src);
         break;
       }
       rest -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    pl.b = b;
-    pl.x = pl.xs - rest;
-    const Tile t = tile_of(p, s, pl.tile);
+    w.x = w.xs - rest;
+    const Tile t = tile_of(p, w.s, w.tile);
     const int cutblk = blocks_before(rest, t.nblk, t.unit);
-    const long long before = me > 0 ? total * (me - 1) / shares : 0;
-    cut.valid = me > 0 && cutblk > 0 && cutblk < t.nblk && blocks_before(before - pl.x, t.nblk, t.unit) == 0;
-    cut.b = b;
-    cut.hk = pl.hk;
-    cut.row0 = pl.tile * kItem;
+    cut.valid = me > 0 && cutblk > 0 && cutblk < t.nblk && blocks_before(share_start(each, extra, me - 1) - w.x, t.nblk, t.unit) == 0;
+    cut.b = w.b;
+    cut.hk = w.hk;
+    cut.row0 = w.tile * kItem;
     cut.rows = t.rows;
-    cut.first = s.row0;
-    cut.n_new = s.n_new;
-    cut.len = s.len;
+    cut.first = w.s.row0;
+    cut.n_new = w.s.n_new;
+    cut.len = w.s.len;
     cut.nblk = t.nblk;
     cut.unit = t.unit;
-    cut.shares = shares;
-    cut.x0 = pl.x;
-    cut.total = total;
+    cut.x0 = w.x;
+    cut.each = each;
+    cut.extra = extra;
   }
+  Piece pc;
+  w.next(p, pc);
   if (lane == 0) {
-    plan = pl;
+    walk = w;
+    first = pc;
     reinterpret_cast<Work*>(p.ws)->cuts[me] = cut;
   }
 }
-
-// Walks the pieces of this CTA's share (warp 0).
-struct Walk {
-  long long x, xs, xe;
-  int hk, b, tile;
-  SeqInfo s;
-
-  __device__ __forceinline__ Walk(const KvAttnParams& p, const Plan& pl)
-      : x(pl.x), xs(pl.xs), xe(pl.xe), hk(pl.hk), b(pl.b), tile(pl.tile) {
-    if (xs < xe) s = seq_info(p.kv, b);
-  }
-  __device__ __forceinline__ bool next(const KvAttnParams& p, Piece& pc) {
-    while (x < xe) {
-      while (tile >= tiles_of(p, s)) {
-        tile = 0;
-        if (++b == p.kv.n_seqs) {
-          b = 0;
-          if (++hk == p.kv.n_heads) return false;
-        }
-        s = seq_info(p.kv, b);
-      }
-      const Tile t = tile_of(p, s, tile);
-      const int b0 = blocks_before(xs - x, t.nblk, t.unit), b1 = blocks_before(xe - x, t.nblk, t.unit);
-      const int row0 = tile * kItem;
-      x += t.cost;
-      ++tile;
-      if (b0 < b1) {
-        pc.b = b;
-        pc.hk = hk;
-        pc.row0 = row0;
-        pc.rows = t.rows;
-        pc.s = s;
-        pc.runs = t.runs;
-        pc.ch = t.ch;
-        pc.blk0 = b0;
-        pc.blk1 = b1;
-        pc.slot = b0 > 0 ? 0 : (b1 < t.nblk ? 1 : -1);
-        return true;
-      }
-    }
-    return false;
-  }
-};
 
 __device__ __forceinline__ void st_shared16(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -352,8 +344,9 @@ struct Feed {
     ++i;
   }
 };
-// Warp 0 hands piece number i to the others (pc.blk1 < 0: there are no more).
+// Warp 0 hands piece number i to the others (pc.blk1 < 0: there are no more).  The plan has handed over the first.
 __device__ __forceinline__ bool publish(const KvAttnParams& p, AttnSmem& sm, uint32_t i, const Piece& pc, int lane) {
+  if (i == 0) return true;
   if (i >= kPieces && !wait_all(p, sm, &sm.piece_empty[i % kPieces], ((i / kPieces) & 1) ^ 1)) return false;
   if (lane == 0) {
     sm.pieces[i % kPieces] = pc;
@@ -422,12 +415,12 @@ __device__ __forceinline__ void issue_boxes(const KvAttnParams& p, const CUtenso
 // for warp 1 to clear the values out of sight.
 __device__ __forceinline__ void load_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
   constexpr int kStages = Ring<false>::kStages;
-  Walk w(p, sm.plan);
-  Piece pc;
+  Walk w = sm.walk;
+  Piece pc = sm.pieces[0];
   uint32_t n = 0, raw = 0, last_raw = 0;  // bit st: parity of raw[st]; whether the stage's last block was a partial one
   uint32_t pieces = 0;
   bool ok = true;
-  while (ok && w.next(p, pc)) {
+  for (bool more = pc.blk1 >= 0; ok && more; more = w.next(p, pc)) {
     if (!publish(p, sm, pieces, pc, lane)) {
       ok = false;
       break;
@@ -449,7 +442,6 @@ __device__ __forceinline__ void load_role(const KvAttnParams& p, AttnSmem& sm, c
       last_raw = (last_raw & ~(1u << st)) | ((whole ? 0u : 1u) << st);
     }
   }
-  pc.blk1 = -1;
   if (ok) publish(p, sm, pieces, pc, lane);
   // every copy has landed before the block exits
   for (uint32_t c = n > kStages ? n - kStages : 0; c < n; ++c) {
@@ -521,16 +513,32 @@ __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, i
     const Piece& pc = *next;
     int k_hi = -127, v_hi = -127, k_lo = 127, v_lo = 127;
     const int per_log2 = 7 - p.box_log2;  // boxes of a block
-#pragma unroll 2
-    for (int i = (pc.blk0 << per_log2) + lane; i < (pc.blk1 << per_log2); i += 32) {
-      const int blk = i >> per_log2, box = i & ((1 << per_log2) - 1);
-      const int row = box_row(p, pc, blk, box, box_entry(p, pc, blk, box));
-      if (row < 0) continue;
-      const int k = exponent(kv.k_scale[row >> kv.page_log2]), v = exponent(kv.v_scale[row >> kv.page_log2]);
-      k_hi = max(k_hi, k);
-      v_hi = max(v_hi, v);
-      if (k > -100) k_lo = min(k_lo, k);
-      if (v > -100) v_lo = min(v_lo, v);
+    // four boxes of a lane at a time: their entries, then their scales
+    for (int i0 = (pc.blk0 << per_log2) + lane; i0 < (pc.blk1 << per_log2); i0 += 128) {
+      int id[4];
+      float ks[4], vs[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int i = i0 + 32 * c;
+        id[c] = box_entry(p, pc, i >> per_log2, i & ((1 << per_log2) - 1));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int i = i0 + 32 * c, row = box_row(p, pc, i >> per_log2, i & ((1 << per_log2) - 1), id[c]);
+        ks[c] = vs[c] = 0.f;
+        if (row >= 0) {
+          ks[c] = kv.k_scale[row >> kv.page_log2];
+          vs[c] = kv.v_scale[row >> kv.page_log2];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = exponent(ks[c]), v = exponent(vs[c]);
+        k_hi = max(k_hi, k);
+        v_hi = max(v_hi, v);
+        if (k > -100) k_lo = min(k_lo, k);
+        if (v > -100) v_lo = min(v_lo, v);
+      }
     }
     k_hi = __reduce_max_sync(0xffffffffu, k_hi);
     v_hi = __reduce_max_sync(0xffffffffu, v_hi);
@@ -548,11 +556,11 @@ __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, i
 __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
   constexpr int kStages = Ring<true>::kStages, kRaw = Ring<true>::kRaw;
   const KvView& kv = p.kv;
-  Walk w(p, sm.plan);
-  Piece pc;
+  Walk w = sm.walk;
+  Piece pc = sm.pieces[0];
   uint32_t n = 0, pieces = 0;
   bool ok = true;
-  while (ok && w.next(p, pc)) {
+  for (bool more = pc.blk1 >= 0; ok && more; more = w.next(p, pc)) {
     if (!publish(p, sm, pieces, pc, lane)) {
       ok = false;
       break;
@@ -594,7 +602,6 @@ __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem&
     }
     ++pieces;
   }
-  pc.blk1 = -1;
   if (ok) publish(p, sm, pieces, pc, lane);
   for (uint32_t c = n > kRaw ? n - kRaw : 0; c < n; ++c) mbar_wait_drain(&sm.raw[c % kRaw], (c / kRaw) & 1, kDrainBudget);
 }
@@ -849,6 +856,12 @@ __device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, f
   return (rp[0] + rp[1]) + (rp[2] + rp[3]);
 }
 
+__device__ __forceinline__ const uint16_t* query_row(const KvAttnParams& p, const Piece& pc, int row) {
+  const int a = pc.row0 + row, tok = p.by_group.div(a), head = pc.hk * p.group + a - tok * p.group;
+  return p.q + (pc.s.row0 + tok) * p.q_ts + head * p.q_hs;
+}
+__device__ __forceinline__ void prefetch_row(const void* src) { asm volatile("prefetch.global.L1 [%0];" ::"l"(src)); }
+
 // Half h of query row t * 128 + r of a piece, the tile's number i (by its softmax thread; the whole warp runs).  8-bit: as
 // fp16 times a power of two of the row (the row's largest has exponent 0; values below 2^-14 of it lose bits, 2^-25 of it
 // at most).
@@ -864,8 +877,7 @@ __device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, 
     for (int c = 0; c < 4; ++c) x[c] = make_uint4(0, 0, 0, 0);
     uint32_t mx = 0;
     if (row < pc.rows) {
-      const int a = pc.row0 + row, tok = a / p.group, head = pc.hk * p.group + a - tok * p.group;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (pc.s.row0 + tok) * p.q_ts + head * p.q_hs);
+      const uint4* src = reinterpret_cast<const uint4*>(query_row(p, pc, row));
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = src[4 * h + c];
       if (kF16) {
@@ -925,7 +937,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       feed.done(sm, lane);
       continue;
     }
-    const int a = pc.row0 + min(t * 128 + r, pc.rows - 1), tok = a / p.group;
+    const int a = pc.row0 + min(t * 128 + r, pc.rows - 1), tok = p.by_group.div(a);
     const Span sp = span_of(p.win, pc.s.len - pc.s.n_new + tok, pc.s.len);
     float m = -INFINITY, l = 0.f;
     bool unset = false;  // some row of the warp has no reference yet
@@ -942,6 +954,10 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       if (!all) {
         valid = have ? range_bits(sp.lo - j0, sp.hi - j0) | range_bits(0, sp.sink - j0) : 0ull;
         part |= have && !whole;
+      }
+      if (blk + 2 == blk1 && mbar_try_wait(&sm.piece_full[(feed.i + 1) % kPieces], ((feed.i + 1) / kPieces) & 1)) {
+        const Piece& nx = sm.pieces[(feed.i + 1) % kPieces];  // its queries, on their way to the caches
+        if (nx.blk1 >= 0 && t * 128 + r < nx.rows) prefetch_row(query_row(p, nx, t * 128 + r));
       }
       if (!wait_all(p, sm, &sm.s_full[t][h], sfull & 1)) return;
       ++sfull;
@@ -1062,7 +1078,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
   extern __shared__ uint8_t smem_raw[];
   AttnSmem& sm = *reinterpret_cast<AttnSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 96) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sm.full[s], kE4m3 ? kConverters : 2);
       mbar_init(&sm.empty[s], 2);
@@ -1088,11 +1104,13 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
     sm.abort = 0;
     fence_mbar_init();
   }
-  make_plan(p, sm.plan, reinterpret_cast<long long*>(sm.ring));  // the ring is not in use yet
   if (warp == 3) {
+    __syncwarp();
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  make_plan(p, sm.walk, sm.pieces[0], reinterpret_cast<long long*>(sm.ring));  // the ring is not in use yet
+  if (threadIdx.x == 0) mbar_arrive(&sm.piece_full[0]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1150,7 +1168,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
   int b0 = 0;
   for (int c = blockIdx.x; b0 < cut.nblk; ++c) {
-    const int b1 = blocks_before(cut.total * (c + 1) / cut.shares - cut.x0, cut.nblk, cut.unit);
+    const int b1 = blocks_before(share_start(cut.each, cut.extra, c + 1) - cut.x0, cut.nblk, cut.unit);
     if (b1 > b0) {
       const Slot& sl = wk.slots[c][b0 > 0 ? 0 : 1];
       const float m = sl.m[r], nm = fmaxf(mm, m);
@@ -1177,7 +1195,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
   const bool live = r < cut.rows;
   uint32_t todo = __ballot_sync(0xffffffffu, live && ((bad && part) || wild));
   const bool mine = ((todo >> (lane & 24)) & 0xffu) != 0;
-  const int a = cut.row0 + r, tok = a / p.group, head = cut.hk * p.group + a - tok * p.group;
+  const int a = cut.row0 + r, tok = p.by_group.div(a), head = cut.hk * p.group + a - tok * p.group;
   if (live && !mine) {
     const long long at = (cut.first + tok) * p.out_ts + head * p.out_hs + col;
     if (p.out_fp32) {

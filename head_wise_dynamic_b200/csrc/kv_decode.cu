@@ -122,7 +122,7 @@ __device__ __forceinline__ Item item_of(const KvAttnParams& p, int y, int z) {
 }
 
 __device__ __forceinline__ void store_row(const KvAttnParams& p, const Item& it, int r, int col, const float* o, float inv) {
-  const int i = it.r0 + r, tok = i / p.group, head = it.hk * p.group + i % p.group;
+  const int i = it.r0 + r, tok = p.by_group.div(i), head = it.hk * p.group + i % p.group;
   const long long at = (it.s.row0 + tok) * p.out_ts + head * p.out_hs + col;
   if (p.out_fp32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
@@ -137,7 +137,7 @@ __device__ __forceinline__ void store_row(const KvAttnParams& p, const Item& it,
 
 __device__ __forceinline__ void exact_item(const KvAttnParams& p, const Item& it, int warp, int lane) {
   for (int r = warp; r < it.rows; r += kWarps) {
-    const int i = it.r0 + r, tok = i / p.group;
+    const int i = it.r0 + r, tok = p.by_group.div(i);
     exact_row(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i % p.group, lane, 0,
               kD);
   }
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const __grid_consta
   const Item it = item_of(p, blockIdx.y, blockIdx.z);
   if (it.rows <= 0) return;
   const int pos0 = it.s.len - it.s.n_new;
-  const int pa = pos0 + it.r0 / p.group, pz = pos0 + (it.r0 + it.rows - 1) / p.group;
+  const int pa = pos0 + p.by_group.div(it.r0), pz = pos0 + p.by_group.div(it.r0 + it.rows - 1);
   const Span sa = span_of(p.win, pa, it.s.len), sz = span_of(p.win, pz, it.s.len);
   const Runs runs = runs_of(sa.lo, sz.hi, sz.sink);
   const Chunks ch = chunks_of(runs);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const __grid_consta
     uint4 u = make_uint4(0, 0, 0, 0), w = u;
     if (r < it.rows) {
       const int a = it.r0 + r;
-      const uint4* q = reinterpret_cast<const uint4*>(p.q + (it.s.row0 + a / p.group) * p.q_ts +
+      const uint4* q = reinterpret_cast<const uint4*>(p.q + (it.s.row0 + p.by_group.div(a)) * p.q_ts +
                                                       (it.hk * p.group + a % p.group) * p.q_hs + 16 * t);
       u = q[0];
       w = q[1];
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const __grid_consta
     }
   }
   // what rows g and g + 8 see
-  const Span sg = span_of(p.win, pos0 + (it.r0 + min(g, it.rows - 1)) / p.group, it.s.len);
-  const Span sh = span_of(p.win, pos0 + (it.r0 + min(g + 8, it.rows - 1)) / p.group, it.s.len);
+  const Span sg = span_of(p.win, pos0 + p.by_group.div(it.r0 + min(g, it.rows - 1)), it.s.len);
+  const Span sh = span_of(p.win, pos0 + p.by_group.div(it.r0 + min(g + 8, it.rows - 1)), it.s.len);
 
   float o[8][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -438,8 +438,8 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const __grid_c
   const Item it = item_of(p, blockIdx.x, blockIdx.y);
   if (it.rows <= 0) return;
   const int pos0 = it.s.len - it.s.n_new;
-  const Span sa = span_of(p.win, pos0 + it.r0 / p.group, it.s.len);
-  const Span sz = span_of(p.win, pos0 + (it.r0 + it.rows - 1) / p.group, it.s.len);
+  const Span sa = span_of(p.win, pos0 + p.by_group.div(it.r0), it.s.len);
+  const Span sz = span_of(p.win, pos0 + p.by_group.div(it.r0 + it.rows - 1), it.s.len);
   const Chunks ch = chunks_of(runs_of(sa.lo, sz.hi, sz.sink));
   if (ch.total <= cps) return;
   const int n = (ch.total + cps - 1) / cps;

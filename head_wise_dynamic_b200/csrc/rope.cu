@@ -5,13 +5,14 @@
 // pairs (8 of the 64 dims), computes their sines and cosines once and walks a chunk of the heads
 // with them, four heads' loads in flight.  32 tokens per block: a warp moves four whole rows per step.
 #include <cmath>
+#include <cstring>
 
 #include "stream.h"
 
 namespace saf3r {
 
-bool build_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t) {
-  if (!cfg || cfg->n_axes < 1 || cfg->n_axes > 4) return false;
+static bool compute_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t) {
+  if (cfg->n_axes < 1 || cfg->n_axes > 4) return false;
   if (cfg->pairing != SAF3R_ROPE_HALF && cfg->pairing != SAF3R_ROPE_PAIRS && cfg->pairing != SAF3R_ROPE_SECTIONS)
     return false;
   if (!(cfg->base >= 1.0 && cfg->base <= 1e12)) return false;
@@ -55,6 +56,24 @@ bool build_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t) {
     t->o1[g] = static_cast<int8_t>(8 * g);
     t->o2[g] = static_cast<int8_t>(8 * g + 4);
   }
+  return true;
+}
+
+// The 32 frequencies take 10 us of the host's time, more than a small call's kernel: the table of this host thread's
+// last configuration is kept, by the configuration's values.
+bool build_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t) {
+  thread_local saf3r_rope_cfg last{};
+  thread_local RopeTable table;
+  thread_local bool have = false;
+  if (!cfg) return false;
+  if (have && std::memcmp(cfg, &last, sizeof(last)) == 0) {
+    *t = table;
+    return true;
+  }
+  if (!compute_rope_table(cfg, t)) return false;
+  last = *cfg;
+  table = *t;
+  have = true;
   return true;
 }
 

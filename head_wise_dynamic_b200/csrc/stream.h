@@ -55,8 +55,31 @@ struct AppendParams {
   const int32_t* pos;
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^l >= d > 2^(l-1), q = (t + ((n - t) >> s1)) >> s2, t the upper half
+// of n * mul, mul = floor(2^32 (2^l - d) / d) + 1 (Granlund and Montgomery, "Division by invariant integers using
+// multiplication").  The attention kernels divide by two numbers of the call, and a division waits 10 times as long.
+struct FastDiv {
+  uint32_t mul, s1, s2;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const {
+    const uint32_t t = __umulhi(mul, static_cast<uint32_t>(n));
+    return static_cast<int>((t + ((static_cast<uint32_t>(n) - t) >> s1)) >> s2);
+  }
+#endif
+};
+inline FastDiv make_div(int32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < static_cast<uint64_t>(d)) ++l;
+  FastDiv f;
+  f.mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << l) - static_cast<uint64_t>(d))) / static_cast<uint64_t>(d) + 1);
+  f.s1 = l > 1 ? 1 : l;
+  f.s2 = l > 1 ? l - 1 : 0;
+  return f;
+}
+
 struct WindowMask {
   int32_t view, window, sink, causal;
+  FastDiv by_view;
 };
 
 struct KvAttnParams {
@@ -68,6 +91,7 @@ struct KvAttnParams {
   void* out;
   long long q_ts, q_hs, out_ts, out_hs;
   int32_t n_heads, group, out_fp32;
+  FastDiv by_group;
   int32_t e4m3;
   uint8_t* ws;
   int32_t num_sms;
@@ -105,7 +129,7 @@ struct Span {
   int lo, hi, sink;
 };
 __device__ __forceinline__ Span span_of(const WindowMask& w, int p, int len) {
-  const long long f = p / w.view;
+  const long long f = w.by_view.div(p);
   Span s;
   s.lo = 0;
   if (w.window > 0 && f - w.window + 1 > 0) s.lo = static_cast<int>((f - w.window + 1) * w.view);

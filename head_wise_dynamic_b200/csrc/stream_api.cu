@@ -79,7 +79,7 @@ KvView view_of(const saf3r_kv_cache* c, const saf3r_kv_batch* b, int* err) {
   return v;
 }
 
-WindowMask mask_of(const saf3r_window* w) { return WindowMask{w->view_tokens, w->window, w->n_sink, w->causal != 0}; }
+WindowMask mask_of(const saf3r_window* w) { return WindowMask{w->view_tokens, w->window, w->n_sink, w->causal != 0, make_div(w->view_tokens)}; }
 
 saf3r_status device(int* sms, int** err) {
   int major = 0;
@@ -208,6 +208,7 @@ saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* ba
   p.out_hs = rows->out_head_stride;
   p.n_heads = rows->n_heads;
   p.group = rows->n_heads / cache->n_heads;
+  p.by_group = make_div(p.group);
   p.out_fp32 = rows->out_is_fp32 != 0;
   p.e4m3 = cache->type == SAF3R_KV_E4M3;
   p.ws = static_cast<uint8_t*>(workspace);
@@ -255,6 +256,7 @@ saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* w
   p.q_hs = p.out_hs = static_cast<long long>(d.N) * kD;
   p.n_heads = d.H;
   p.group = 1;
+  p.by_group = make_div(1);
   p.out_fp32 = out_is_fp32 != 0;
   p.ws = static_cast<uint8_t*>(workspace);
   p.num_sms = sms;

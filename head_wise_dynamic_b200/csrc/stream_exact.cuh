@@ -30,7 +30,7 @@ __device__ __forceinline__ long long kv_row(const KvAttnParams& p, int b, int hk
 // Run by one warp: token `row` of the step's tensors, at position pos of sequence b.  Writes columns c0..c1-1.
 static __device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int len, int row, int pos, int head, int lane, int c0,
                                        int c1) {
-  const int hk = head / p.group;
+  const int hk = p.by_group.div(head);
   const Span sp = span_of(p.win, pos, len);
   const uint16_t* q = p.q + row * p.q_ts + head * p.q_hs;
   float m = -INFINITY, l = 0.f, a0 = 0.f, a1 = 0.f;

@@ -90,6 +90,8 @@ def make_window(view_tokens: int = 1, window: int = 0, n_sink: int = 0, causal: 
 
 
 # ------------------------------------------------------------------ checks
+#
+# A small step's call is as long as its checks: they compare first and word an error only when there is one.
 
 def _need(ok: bool, what: str):
     if not ok:
@@ -98,49 +100,45 @@ def _need(ok: bool, what: str):
 
 def _dense(t, dtype, shape, device, what: str):
     """A contiguous tensor of this type, shape and device: its address."""
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous() and t.device == device,
-          f"{what}: a contiguous {dtype} tensor {tuple(shape)} on {device} is wanted, "
-          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor {tuple(shape)} on {device} is wanted, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _row_strides(t, tokens: int, heads: int, device, what: str):
     """A [tokens, heads, 64] tensor in any order of its rows: its token and head strides."""
-    shape = t.shape
-    _need(len(shape) == 3 and shape[0] == tokens and shape[1] == heads and shape[2] == 64 and t.device == device,
-          f"{what}: a tensor [{tokens}, {heads}, 64] on {device} is wanted, got {tuple(shape)} on {t.device}")
+    if t.shape != (tokens, heads, 64) or t.device != device:
+        raise ValueError(f"{what}: a tensor [{tokens}, {heads}, 64] on {device} is wanted, got {tuple(t.shape)} on {t.device}")
     a, b, c = t.stride()
-    _need(c == 1, f"{what}: the last dimension must be contiguous")
+    if c != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
     # the stride of a dimension of one says nothing: any valid one will do
     return (a if tokens > 1 else 64), (b if heads > 1 else 64)
 
 
 def _workspace(t, n: int, device):
-    _need(t.is_contiguous() and t.device == device and t.numel() * t.element_size() >= n,
-          f"workspace: a contiguous tensor of at least {n} bytes on {device} is wanted")
+    if t.device != device or t.numel() * t.element_size() < n or not t.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor of at least {n} bytes on {device} is wanted")
+    return t.data_ptr()
 
 
-class _on:
-    """Makes a tensor's device the current one for a call, and gives the stream to use."""
-
-    def __init__(self, device, stream):
-        import torch
-        _need(device.type == "cuda", f"a CUDA tensor is wanted, got one on {device}")
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        import torch
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        return self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _launch(device, stream, call, *args):
+    """call(*args, stream) with the tensors' device as the current one; without `stream` on torch's current stream."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"CUDA tensors are wanted, got some on {device}")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, stream)
+    if status:
+        _hw._check(status, call.__name__)
 
 
 # ------------------------------------------------------------------ handles
@@ -164,6 +162,7 @@ class PagedKV:
             sk = _dense(k_scale, torch.float32, k.shape[:2], k.device, "k_scale")
             sv = _dense(v_scale, torch.float32, k.shape[:2], k.device, "v_scale")
         self.c = saf3r_kv_cache(self.n_pages, self.n_heads, self.page, KV_E4M3 if eight else KV_BF16, kp, vp, sk, sv)
+        self.ref = _ref(self.c)
 
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, page: int = 64, kv_type: int = KV_E4M3, device="cuda") -> "PagedKV":
@@ -193,6 +192,7 @@ class KVBatch:
             _dense(cu_tokens, torch.int32, (n + 1,), self.device, "cu_tokens"),
             _dense(kv_lens, torch.int32, (n,), self.device, "kv_lens"),
             _dense(page_table, torch.int32, (n, page_table.shape[1]), self.device, "page_table"))
+        self.ref = _ref(self.c)
 
 
 # ------------------------------------------------------------------ the calls
@@ -203,14 +203,13 @@ def saf3r_rope(rope, x, pos, out, n_rot_heads: Optional[int] = None, inverse: bo
     in any order (out may be a transposed head-major tensor).  inverse: the adjoint."""
     import torch
     T, H, dev = x.shape[0], x.shape[1], x.device
-    fp32 = {torch.float32: 1, torch.bfloat16: 0}
-    _need(x.dtype in fp32 and out.dtype in fp32, "x and out: bfloat16 or float32")
-    xs, os = _row_strides(x, T, H, dev, "x"), _row_strides(out, T, H, dev, "out")
-    pp = _dense(pos, torch.int32, (T, rope.n_axes), dev, "pos")
-    a = saf3r_rope_args(T, H, H if n_rot_heads is None else int(n_rot_heads), x.data_ptr(), xs[0], xs[1],
-                        out.data_ptr(), os[0], os[1], fp32[x.dtype], fp32[out.dtype], pp, int(bool(inverse)))
-    with _on(dev, stream) as st:
-        _hw._check(_hw.lib().saf3r_rope(_ref(rope), _ref(a), st), "saf3r_rope")
+    xf, of = x.dtype == torch.float32, out.dtype == torch.float32
+    _need((xf or x.dtype == torch.bfloat16) and (of or out.dtype == torch.bfloat16), "x and out: bfloat16 or float32")
+    xt, xh = _row_strides(x, T, H, dev, "x")
+    ot, oh = _row_strides(out, T, H, dev, "out")
+    a = saf3r_rope_args(T, H, H if n_rot_heads is None else int(n_rot_heads), x.data_ptr(), xt, xh, out.data_ptr(), ot, oh,
+                        xf, of, _dense(pos, torch.int32, (T, rope.n_axes), dev, "pos"), bool(inverse))
+    _launch(dev, stream, _hw.lib().saf3r_rope, _ref(rope), _ref(a))
 
 
 def saf3r_kv_append(cache: PagedKV, batch: KVBatch, k, v, rope=None, pos=None, stream=None):
@@ -220,20 +219,19 @@ def saf3r_kv_append(cache: PagedKV, batch: KVBatch, k, v, rope=None, pos=None, s
     dev, T, H = cache.device, batch.n_tokens, cache.n_heads
     _need(batch.device == dev and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16,
           "k and v: bfloat16 tensors, the batch on the cache's device")
-    ks, vs = _row_strides(k, T, H, dev, "k"), _row_strides(v, T, H, dev, "v")
+    kt, kh = _row_strides(k, T, H, dev, "k")
+    vt, vh = _row_strides(v, T, H, dev, "v")
     pp = None
     if rope is not None:
         _need(pos is not None, "a rope needs pos")
         pp = _dense(pos, torch.int32, (T, rope.n_axes), dev, "pos")
-    a = saf3r_kv_rows(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], pp)
-    with _on(dev, stream) as st:
-        _hw._check(_hw.lib().saf3r_kv_append(_ref(cache.c), _ref(batch.c), None if rope is None else _ref(rope),
-                                             _ref(a), st), "saf3r_kv_append")
+    a = saf3r_kv_rows(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, pp)
+    _launch(dev, stream, _hw.lib().saf3r_kv_append, cache.ref, batch.ref, None if rope is None else _ref(rope), _ref(a))
 
 
 def saf3r_kv_attn_workspace_bytes(cache: PagedKV, batch: KVBatch, window: saf3r_window, n_heads: int) -> int:
     """Workspace bytes of saf3r_kv_attn for n_heads query heads (ValueError for sizes it does not take)."""
-    n = int(_hw.lib().saf3r_kv_attn_workspace_bytes(_ref(cache.c), _ref(batch.c), _ref(window), int(n_heads)))
+    n = int(_hw.lib().saf3r_kv_attn_workspace_bytes(cache.ref, batch.ref, _ref(window), int(n_heads)))
     _need(n > 0, "sizes that saf3r_kv_attn does not take")
     return n
 
@@ -246,12 +244,11 @@ def saf3r_kv_attn(cache: PagedKV, batch: KVBatch, window: saf3r_window, q, out, 
     fp32 = out.dtype == torch.float32
     _need(batch.device == dev and q.dtype == torch.bfloat16 and (fp32 or out.dtype == torch.bfloat16),
           "q: bfloat16, out: bfloat16 or float32, the batch on the cache's device")
-    qs, os = _row_strides(q, T, H, dev, "q"), _row_strides(out, T, H, dev, "out")
-    _workspace(workspace, saf3r_kv_attn_workspace_bytes(cache, batch, window, H), dev)
-    a = saf3r_query_rows(H, int(fp32), q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1])
-    with _on(dev, stream) as st:
-        _hw._check(_hw.lib().saf3r_kv_attn(_ref(cache.c), _ref(batch.c), _ref(window), _ref(a), workspace.data_ptr(), st),
-                   "saf3r_kv_attn")
+    qt, qh = _row_strides(q, T, H, dev, "q")
+    ot, oh = _row_strides(out, T, H, dev, "out")
+    ws = _workspace(workspace, saf3r_kv_attn_workspace_bytes(cache, batch, window, H), dev)
+    a = saf3r_query_rows(H, fp32, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh)
+    _launch(dev, stream, _hw.lib().saf3r_kv_attn, cache.ref, batch.ref, _ref(window), _ref(a), ws)
 
 
 def saf3r_window_attn_workspace_bytes(layout, window: saf3r_window) -> int:
@@ -267,9 +264,7 @@ def saf3r_window_attn(layout, window: saf3r_window, q, k, v, out, workspace, str
     L = _hw.layout_of(layout)
     dev, shape = q.device, (L.H, L.S * (L.grid_h * L.grid_w + L.n_special), L.d)
     fp32 = out.dtype == torch.float32
-    ptrs = [_dense(t, torch.bfloat16, shape, dev, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    ptrs.append(_dense(out, torch.float32 if fp32 else torch.bfloat16, shape, dev, "out"))
-    _workspace(workspace, saf3r_window_attn_workspace_bytes(L, window), dev)
-    with _on(dev, stream) as st:
-        _hw._check(_hw.lib().saf3r_window_attn(_ref(L), _ref(window), *ptrs, int(fp32), workspace.data_ptr(), st),
-                   "saf3r_window_attn")
+    qp, kp, vp = (_dense(t, torch.bfloat16, shape, dev, n) for t, n in ((q, "q"), (k, "k"), (v, "v")))
+    op = _dense(out, torch.float32 if fp32 else torch.bfloat16, shape, dev, "out")
+    ws = _workspace(workspace, saf3r_window_attn_workspace_bytes(L, window), dev)
+    _launch(dev, stream, _hw.lib().saf3r_window_attn, _ref(L), _ref(window), qp, kp, vp, op, fp32, ws)
