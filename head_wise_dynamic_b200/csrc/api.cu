@@ -727,8 +727,8 @@ bool saf3r::make_map_rows(CUtensorMap* m, const void* base, long long rows, long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [rows][64] 8-bit codes, box_rows x 64 boxes, as they are.
-bool saf3r::make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows) {
+// [rows][64] 8-bit codes, box_rows x 64 boxes, as they are or with 64-byte swizzle.
+bool saf3r::make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 1};
@@ -736,8 +736,8 @@ bool saf3r::make_map_codes(CUtensorMap* m, const void* base, long long rows, int
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ======================================================================== C ABI

@@ -1232,7 +1232,7 @@ saf3r_status launch_attn(const KvAttnParams& p0, cudaStream_t stream, int* n_lau
     p.box_log2 = kv.page_log2 < 6 ? kv.page_log2 : 6;
     const int box = 1 << p.box_log2;
     const long long rows = static_cast<long long>(kv.n_pages) * kv.n_heads * kv.page;
-    ok = p.e4m3 ? make_map_codes(&mk, kv.k, rows, box) && make_map_codes(&mv, kv.v, rows, box)
+    ok = p.e4m3 ? make_map_codes(&mk, kv.k, rows, box, false) && make_map_codes(&mv, kv.v, rows, box, false)
                 : make_map_rows(&mk, kv.k, rows, kD, 1, rows * kD, box) && make_map_rows(&mv, kv.v, rows, kD, 1, rows * kD, box);
   }
   if (!ok) return SAF3R_ERR_CUDA;

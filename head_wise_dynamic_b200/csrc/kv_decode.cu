@@ -1,22 +1,25 @@
 // Attention of a few query rows per sequence over the paged cache (single tokens and short chunks).
 //
-// Bound by memory: every visible key and value row is read once per kv head and 16 query rows (the
-// heads of a group times the new tokens).  The keys of an item (sequence, kv head, 16 rows) are split
-// into pieces for the GPU's SMs; a piece is four warps that take chunks of keys in turn, each with
-// its own running maximum and sum, merged in shared memory and, over pieces, by a second small kernel.
+// Bound by memory: every visible key and value row is read once per kv head and 8 or 16 query rows (the heads of a
+// group times the new tokens).  An item is those rows of one sequence and kv head; the items' chunks of 64
+// keys, laid end to end, are cut into equal shares, one for each warp, so that unequal lengths and few
+// streams keep every SM reading alike.  An item cut by a share's border is finished by a second small kernel.
 //
-// Fragments come straight from global memory, with no shared memory in between.  The matrix
-// products may contract their 64 dims, and number their value columns, in any order, so the
-// order is chosen for the loads: in Q K^T lane (g, t) of the m16n8k16 B fragment takes the 16 dims
-// 16t.. of key g (one 16-byte load of an 8-bit row, two of a bf16 one: a warp reads whole rows), and in P V
-// value column n of tile nt is dim 8n + nt, so a lane needs 8 dims in a row of each of its keys.
-// An output row's lane then owns dims 16t..16t+15.
+// A warp streams its keys 8 KB at a time (64 keys of 8 bits, 32 of bf16) through two TMA buffers of its own: one is
+// in flight while the other is worked on.  The products are transposed, S^T = K Q^T and O^T = V^T P^T: the keys
+// are the 16 rows of m16n8k16 and 8 query rows its columns, which halves the work against 16 rows when
+// there are 8 or fewer.  The 64 dims may be contracted in any order, and the rows of O^T may be any dims: lane (g, t)
+// takes the 16 dims 16t.. of its keys and the 8 dims 8g.. of its values.  Keys g of a group of 16 stand for its keys
+// sigma(g), which with the tensor map's swizzle makes every shared load free of bank conflicts.
 //
 // 8-bit caches: codes become fp16 exactly (one conversion for two) and Q is scaled by a power of
-// two per row so that it fits fp16 (its 8 significant bits do, down to 2^-24 of the row's largest); the page's key scale
-// multiplies the fp32 logits.  The value scale goes into the exponent: with x = s + log2(vs), P = 2^(x - max x)
-// is the weight times vs, at most 1, whatever the scales' range, and the sum takes P / vs.  bf16
-// caches use bf16 products; P is rounded to bf16 there (2^-9 relative, as the tensor-core kernels do).
+// two per row so that it fits fp16 (its 8 significant bits do, down to 2^-24 of the row's largest).  The page's key
+// scale multiplies the fp32 logits.  Its value scale goes into the exponent: with x = s + log2(vs), P = 2^(x - reference)
+// is the weight times vs, and the row's sum takes P / vs.  bf16 caches use bf16 products throughout.
+// The reference is the largest x of the first step; it moves when a later one exceeds it by 2^15
+// (fp16 P, which ends 2^-24 below it) or 2^24.
+#include <cuda.h>
+
 #include "ptx.cuh"
 #include "stream.h"
 #include "stream_exact.cuh"
@@ -25,8 +28,13 @@ namespace saf3r {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kRows = 16;
+constexpr int kWarps = 4;              // of a block
+constexpr int kBlocksPerSm = 3;        // 64 KB of shared memory and at most 168 registers a thread
+constexpr int kMaxRows = 16;
+constexpr int kStepBytes = 8192;       // of keys and values
+constexpr int kMaxShares = 160 * kBlocksPerSm * kWarps;
+constexpr int kCostItem = 1;           // an item's start and end, in chunks
+constexpr int kWild = 64;              // largest spread of value scales (in exponents) that a row's fp32 sum is sure to bear
 constexpr float kLog2Scale = 0.18033688011112042f;  // log2(e) / sqrt(64)
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -39,6 +47,12 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// an 8 x 8 matrix of 16-bit values across the warp, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
 __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
@@ -49,470 +63,661 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-template <typename T>
-__device__ __forceinline__ T load_stream(const void* p) {
-  return __ldcs(static_cast<const T*>(p));
-}
 
-// Chunks of a whole sequence's new tokens (what its items read, at most).
-__device__ __forceinline__ int seq_chunks(const WindowMask& w, const SeqInfo& s) {
-  if (s.n_new <= 0) return 0;
-  const Span a = span_of(w, s.len - s.n_new, s.len), z = span_of(w, s.len - 1, s.len);
-  return chunks_of(runs_of(a.lo, z.hi, z.sink)).total;
-}
-
-// Chunks per piece for this call.  Run by a whole block; every block finds the same value.
-__device__ __forceinline__ int chunks_per_piece(const KvAttnParams& p, int groups, int* scratch) {
-  const KvView& kv = p.kv;
-  int most = 0;
-  long long sum = 0;
-  for (int b = threadIdx.x; b < kv.n_seqs; b += blockDim.x) {
-    const int c = seq_chunks(p.win, seq_info(kv, b));
-    most = max(most, c);
-    sum += c;
-  }
-  int isum = static_cast<int>(min(sum, 1LL << 24));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-    isum += __shfl_xor_sync(0xffffffffu, isum, d);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    scratch[2 * (threadIdx.x >> 5)] = most;
-    scratch[2 * (threadIdx.x >> 5) + 1] = isum;
-  }
-  __syncthreads();
-  sum = 0;
-  for (int w = 0; w < (blockDim.x >> 5); ++w) {
-    most = max(most, scratch[2 * w]);
-    sum += scratch[2 * w + 1];
-  }
-  sum *= kv.n_heads * groups;
-  const long long target = 8LL * p.num_sms;  // pieces wanted: two rounds of four blocks per SM
-  long long cps = (sum + target - 1) / target;
-  cps = max(cps, static_cast<long long>((most + p.n_split - 1) / p.n_split));
-  return static_cast<int>(max(cps, static_cast<long long>(kWarps)));
-}
-
-struct Stats {
-  float m[kRows], l[kRows];
-  int bad;  // a value that some rows must not see is not finite
-  int pad[3];
+// A warp's part of an item that a border cuts: per row the part's answer, log2 of the sum of its weights, and flags.
+struct Slot {
+  float o[kMaxRows][kD];
+  float w[kMaxRows];
+  int32_t flags[kMaxRows];  // 1: some streamed key is out of the row's sight, 2: value scales too far apart
 };
-constexpr size_t kPieceBytes = kRows * kD * sizeof(float) + sizeof(Stats);
-static_assert(kPieceBytes % 16 == 0, "pieces stay aligned");
+// Where an item lies on the line of all chunks (written by the warp that begins it).
+struct ItemRec {
+  long long x0;
+  int32_t chunks, pad;
+};
 
-__device__ __forceinline__ uint8_t* piece_at(const KvAttnParams& p, long long item, int s) {
-  return p.ws + (item * p.n_split + s) * kPieceBytes;
+struct Share {
+  long long each;
+  int32_t extra, shares;
+};
+__device__ __forceinline__ long long share_start(const Share& sh, int i) { return sh.each * i + min(i, sh.extra); }
+__device__ __forceinline__ int share_of(const Share& sh, long long x) {
+  const long long big = (sh.each + 1) * sh.extra;
+  return static_cast<int>(x < big ? x / (sh.each + 1) : sh.extra + (x - big) / sh.each);
 }
 
-// Row r of an item: token and head.  Rows from `rows` on do not exist.
+// Row group rg of a sequence: rows rg * R.. of its (token, group head) rows.
 struct Item {
-  int b, hk, r0, rows;
+  int b, hk, rg, rows;
   SeqInfo s;
+  Runs runs;
+  Chunks ch;
+  Span first, last;  // what the first and the last row see
 };
-__device__ __forceinline__ Item item_of(const KvAttnParams& p, int y, int z) {
+__device__ __forceinline__ int row_groups(const KvAttnParams& p, const SeqInfo& s, int R) {
+  return s.n_new <= 0 ? 0 : (s.n_new * p.group + R - 1) / R;
+}
+__device__ __forceinline__ Item item_of(const KvAttnParams& p, const SeqInfo& s, int b, int hk, int rg, int R) {
   Item it;
-  it.b = z;
-  it.hk = y % p.kv.n_heads;
-  it.r0 = (y / p.kv.n_heads) * kRows;
-  it.s = seq_info(p.kv, z);
-  it.rows = min(kRows, it.s.n_new * p.group - it.r0);
+  it.b = b;
+  it.hk = hk;
+  it.rg = rg;
+  it.s = s;
+  it.rows = min(R, s.n_new * p.group - rg * R);
+  const int pos0 = s.len - s.n_new;
+  it.first = span_of(p.win, pos0 + p.by_group.div(rg * R), s.len);
+  it.last = span_of(p.win, pos0 + p.by_group.div(rg * R + it.rows - 1), s.len);
+  it.runs = runs_of(it.first.lo, it.last.hi, it.last.sink);
+  it.ch = chunks_of(it.runs);
   return it;
 }
+__device__ __forceinline__ long long seq_head_cost(const KvAttnParams& p, const SeqInfo& s, int R) {
+  const int n = row_groups(p, s, R);
+  long long c = 0;
+  for (int rg = 0; rg < n; ++rg) c += item_of(p, s, 0, 0, rg, R).ch.total + kCostItem;
+  return c;
+}
 
-__device__ __forceinline__ void store_row(const KvAttnParams& p, const Item& it, int r, int col, const float* o, float inv) {
-  const int i = it.r0 + r, tok = p.by_group.div(i), head = it.hk * p.group + i % p.group;
+__device__ __forceinline__ long long item_index(const KvAttnParams& p, int b, int hk, int rg, int R) {
+  const int groups = (p.kv.max_new * p.group + R - 1) / R;
+  return (static_cast<long long>(b) * p.kv.n_heads + hk) * groups + rg;
+}
+__device__ __forceinline__ ItemRec* recs(const KvAttnParams& p) { return reinterpret_cast<ItemRec*>(p.ws + sizeof(Share) * 16); }
+__device__ __forceinline__ Slot* slots(const KvAttnParams& p, int R) {
+  const long long items = item_index(p, p.kv.n_seqs, 0, 0, R);
+  return reinterpret_cast<Slot*>(p.ws + sizeof(Share) * 16 + items * sizeof(ItemRec));
+}
+
+// Walks the pieces of a warp's share.
+struct Walk {
+  long long x, xs, xe;
+  int b, hk, rg;
+  SeqInfo s;
+
+  // the next piece: chunks c0 .. c1 - 1 of the item
+  __device__ __forceinline__ bool next(const KvAttnParams& p, int R, Item& it, int& c0, int& c1, long long& x0) {
+    while (x < xe) {
+      while (rg >= row_groups(p, s, R)) {
+        rg = 0;
+        if (++hk >= p.kv.n_heads || s.n_new <= 0) {
+          hk = 0;
+          if (++b >= p.kv.n_seqs) return false;
+          s = seq_info(p.kv, b);
+        }
+      }
+      it = item_of(p, s, b, hk, rg, R);
+      x0 = x;
+      const long long d0 = xs - x, d1 = xe - x;
+      c0 = d0 <= 0 ? 0 : (d0 < it.ch.total ? static_cast<int>(d0) : it.ch.total);
+      c1 = d1 < it.ch.total ? static_cast<int>(d1) : it.ch.total;
+      x += it.ch.total + kCostItem;
+      ++rg;
+      if (c0 < c1) return true;
+    }
+    return false;
+  }
+};
+
+// Finds every warp's share (run by the whole block; each warp gets its own walk).
+__device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long long* entries, Share& sh) {
+  constexpr int kThreads = 32 * kWarps;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.kv.n_seqs;
+  const int per = (n + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int b = threadIdx.x * per; b < min(static_cast<int>(threadIdx.x + 1) * per, n); ++b)
+    mine += seq_head_cost(p, seq_info(p.kv, b), R) * p.kv.n_heads;
+  long long incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  entries[threadIdx.x] = incl;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += entries[32 * w + 31];
+  const int most = gridDim.x * kWarps;
+  sh.shares = total >= static_cast<long long>(most) * p.least_share ? most : max(1, static_cast<int>(total) / p.least_share);
+  sh.each = total / sh.shares;
+  sh.extra = static_cast<int>(total - sh.each * sh.shares);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<Share*>(p.ws) = sh;
+  // neighbouring shares go to different SMs: few streams spread over all of them
+  const int me = warp * gridDim.x + blockIdx.x;
+  Walk w;
+  w.b = w.hk = w.rg = 0;
+  w.s = SeqInfo{0, 0, 0, false};
+  w.xs = me < sh.shares ? share_start(sh, me) : total;
+  w.xe = me < sh.shares ? share_start(sh, me + 1) : total;
+  w.x = w.xs;
+  if (w.xs >= w.xe) return w;
+  long long rest = w.xs;
+  for (int q = 0; q < kWarps; ++q) {
+    const long long in = entries[32 * q + lane];
+    const uint32_t hit = __ballot_sync(0xffffffffu, rest < in);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      w.b = (32 * q + src) * per;
+      if (src > 0) rest -= entries[32 * q + src - 1];
+      break;
+    }
+    rest -= entries[32 * q + 31];
+  }
+  long long head = 0;
+  for (;; ++w.b) {
+    w.s = seq_info(p.kv, w.b);
+    head = seq_head_cost(p, w.s, R);
+    if (per == 1 || w.b + 1 >= n || rest < head * p.kv.n_heads) break;
+    rest -= head * p.kv.n_heads;
+  }
+  while (rest >= head && w.hk + 1 < p.kv.n_heads) {
+    rest -= head;
+    ++w.hk;
+  }
+  const int groups = row_groups(p, w.s, R);
+  while (w.rg + 1 < groups) {
+    const int c = item_of(p, w.s, w.b, w.hk, w.rg, R).ch.total + kCostItem;
+    if (rest < c) break;
+    rest -= c;
+    ++w.rg;
+  }
+  w.x = w.xs - rest;
+  return w;
+}
+
+__device__ __forceinline__ void store8(const KvAttnParams& p, const Item& it, int row, int R, int col, const float* o) {
+  const int i = it.rg * R + row, tok = p.by_group.div(i), head = it.hk * p.group + i - tok * p.group;
   const long long at = (it.s.row0 + tok) * p.out_ts + head * p.out_hs + col;
   if (p.out_fp32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-    d[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-    d[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+    d[0] = make_float4(o[0], o[1], o[2], o[3]);
+    d[1] = make_float4(o[4], o[5], o[6], o[7]);
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
-        make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                   pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+        make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
   }
 }
-
-__device__ __forceinline__ void exact_item(const KvAttnParams& p, const Item& it, int warp, int lane) {
-  for (int r = warp; r < it.rows; r += kWarps) {
-    const int i = it.r0 + r, tok = p.by_group.div(i);
-    exact_row(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i % p.group, lane, 0,
-              kD);
-  }
+__device__ __forceinline__ void exact_item_row(const KvAttnParams& p, const Item& it, int row, int R, int lane) {
+  const int i = it.rg * R + row, tok = p.by_group.div(i);
+  exact_row(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i - tok * p.group, lane, 0, kD);
 }
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(32 * kWarps) decode_kernel(const __grid_constant__ KvAttnParams p) {
-  constexpr int kT = kE4m3 ? 64 : 32;   // keys of one step of a warp: 8 KB of keys and values
-  constexpr int kTiles = kT / 8;
-  __shared__ float s_o[kWarps][kRows][kD + 4];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-  __shared__ int s_scratch[2 * kWarps];
-  __shared__ int s_bad;
+struct DecodeSmem {
+  uint8_t buf[kWarps][2][kStepBytes];
+  uint64_t full[kWarps][2];
+  long long entries[32 * kWarps];
+  int abort;
+};
+
+// kB: tiles of 8 query rows.
+template <bool kE4m3, int kB>
+__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
+    decode_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  constexpr int R = 8 * kB;
+  constexpr int kT = kE4m3 ? 64 : 32;     // keys of a step
+  constexpr int kG = kT / 16;             // groups of 16 keys
+  constexpr int kRowBytes = kE4m3 ? 64 : 128;
+  constexpr int kSteps = 64 / kT;         // steps of a chunk
+  constexpr float kRaise = kE4m3 ? 15.f : 24.f;
+  extern __shared__ uint8_t smem_raw[];
+  DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const KvView& kv = p.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (threadIdx.x == 0) s_bad = 0;
-  const int cps = chunks_per_piece(p, gridDim.y / kv.n_heads, s_scratch);
-  const Item it = item_of(p, blockIdx.y, blockIdx.z);
-  if (it.rows <= 0) return;
-  const int pos0 = it.s.len - it.s.n_new;
-  const int pa = pos0 + p.by_group.div(it.r0), pz = pos0 + p.by_group.div(it.r0 + it.rows - 1);
-  const Span sa = span_of(p.win, pa, it.s.len), sz = span_of(p.win, pz, it.s.len);
-  const Runs runs = runs_of(sa.lo, sz.hi, sz.sink);
-  const Chunks ch = chunks_of(runs);
-  const int c0 = blockIdx.x * cps, c1 = min(c0 + cps, ch.total);
-  if (c0 >= c1) return;
-
-  // Q fragments: rows g and g + 8, dims 16t..16t+15
-  uint32_t qa[4][4];
-  float qs[2] = {kLog2Scale, kLog2Scale};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = g + 8 * i;
-    uint4 u = make_uint4(0, 0, 0, 0), w = u;
-    if (r < it.rows) {
-      const int a = it.r0 + r;
-      const uint4* q = reinterpret_cast<const uint4*>(p.q + (it.s.row0 + p.by_group.div(a)) * p.q_ts +
-                                                      (it.hk * p.group + a % p.group) * p.q_hs + 16 * t);
-      u = q[0];
-      w = q[1];
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kWarps; ++w) {
+      mbar_init(&sm.full[w][0], 1);
+      mbar_init(&sm.full[w][1], 1);
     }
-    uint32_t v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-    if (kE4m3) {
-      // the row's largest exponent; then every value times 2^-e, as fp16
-      uint32_t mx = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = max(mx, max((v[j] >> 7) & 0xffu, (v[j] >> 23) & 0xffu));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = mx == 0xff ? 0 : min(max(static_cast<int>(mx) - 127, -120), 120);  // an infinity or NaN stays one
-      const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      qs[i] = kLog2Scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      qa[kk][i] = v[2 * kk];
-      qa[kk][2 + i] = v[2 * kk + 1];
-    }
+    sm.abort = 0;
+    fence_mbar_init();
   }
-  // what rows g and g + 8 see
-  const Span sg = span_of(p.win, pos0 + p.by_group.div(it.r0 + min(g, it.rows - 1)), it.s.len);
-  const Span sh = span_of(p.win, pos0 + p.by_group.div(it.r0 + min(g + 8, it.rows - 1)), it.s.len);
+  Share sh;
+  Walk walk = make_walk(p, R, sm.entries, sh);  // (syncs the block)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  float o[8][4];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int n = 0; n < 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  bool bad = false;
-  const int32_t* table = kv.table + static_cast<long long>(it.b) * kv.max_pages;
-  constexpr int kSteps = 64 / kT;  // steps of a chunk
-  for (int st = c0 * kSteps + warp; st < c1 * kSteps; st += kWarps) {
-    const int j0 = ch.key(st / kSteps) + (st % kSteps) * kT;
-    // keys of this step that some row sees: [ua, ub) and below ue
-    const int ue = runs.a_end, ua = runs.b_begin, ub = runs.b_end;
-    if (j0 >= ub || (j0 + kT <= ua && j0 >= ue)) continue;
-    const bool whole = (j0 >= sz.lo && j0 + kT <= sa.hi) || j0 + kT <= sa.sink;  // every row sees every key
-    long long base[kT / 16];   // first row of each 16 keys in the pools, -1: not read
-    float ks[kT / 16], lv[kT / 16], vi[kT / 16];
-#pragma unroll
-    for (int i = 0; i < kT / 16; ++i) {
-      const int j = j0 + 16 * i;
-      base[i] = -1;
-      ks[i] = vi[i] = 1.f;
-      lv[i] = 0.f;
-      if (j < ub && (j + 16 > ua || j < ue)) {
-        const int id = table[j >> kv.page_log2];
-        if (id < 0 || id >= kv.n_pages) {
+  uint64_t* full = sm.full[warp];
+  uint32_t issued = 0, used = 0;
+  bool ok = true;
+  // sigma(m): the key of its group of 16 that row m of the products stands for
+  auto sigma = [](int m) { return m ^ ((m >> 1) & 1); };
+  Item it;
+  int c0, c1;
+  long long x0;
+  while (ok && walk.next(p, R, it, c0, c1, x0)) {
+    if (c0 == 0 && lane == 0) recs(p)[item_index(p, it.b, it.hk, it.rg, R)] = ItemRec{x0, it.ch.total, 0};
+    const int n_steps = (c1 - c0) * kSteps;
+    const int32_t* table = kv.table + static_cast<long long>(it.b) * kv.max_pages;
+    auto step_key = [&](int i) { return it.ch.key(c0 + i / kSteps) + (i % kSteps) * kT; };
+    auto seen = [&](int j) { return j < it.runs.b_end && (j >= it.runs.b_begin || j < it.runs.a_end); };
+    // this lane's box of step i: its first key, -1 where there is none to read
+    auto box_key = [&](int i) {
+      if (lane >= (kT >> p.box_log2) || i >= n_steps) return -1;
+      const int j = step_key(i) + (lane << p.box_log2);
+      return j < it.runs.b_end && (j + (1 << p.box_log2) > it.runs.b_begin || j < it.runs.a_end) ? j : -1;
+    };
+    auto box_entry = [&](int i) {
+      const int j = box_key(i);
+      return j >= 0 ? table[j >> kv.page_log2] : 0;
+    };
+    // copies step i, whose page entry is `entry`; returns the scales of this lane's box
+    auto issue = [&](int i, int entry) {
+      const int j = box_key(i);
+      int row = -1;
+      float2 scale = make_float2(1.f, 1.f);
+      if (j >= 0) {
+        if (entry < 0 || entry >= kv.n_pages) {
           atomicCAS(kv.err, 0, SAF3R_ERR_INDEX);
         } else {
-          const long long at = static_cast<long long>(id) * kv.n_heads + it.hk;
-          base[i] = (at << kv.page_log2) + (j & (kv.page - 1));
-          if (kE4m3) {
-            ks[i] = kv.k_scale[at];
-            const float v = kv.v_scale[at];
-            lv[i] = static_cast<float>(static_cast<int>(__float_as_uint(v) >> 23) - 127);
-            vi[i] = __uint_as_float((254u << 23) - (__float_as_uint(v) & 0x7f800000u));
+          const int at = entry * kv.n_heads + it.hk;
+          row = (at << kv.page_log2) + (j & (kv.page - 1));
+          if (kE4m3) scale = make_float2(kv.k_scale[at], kv.v_scale[at]);
+        }
+      }
+      if (i < n_steps) {
+        uint64_t* bar = &full[issued & 1];
+        uint8_t* dst = sm.buf[warp][issued & 1];
+        const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(bar, ((2 * __popc(have)) << p.box_log2) * kRowBytes);
+        __syncwarp();
+        if (row >= 0) {
+          uint8_t* d = dst + (lane << p.box_log2) * kRowBytes;
+          tma_load_3d(d, &map_k, 0, row, 0, bar);
+          tma_load_3d(d + kStepBytes / 2, &map_v, 0, row, 0, bar);
+        }
+        __syncwarp();
+        ++issued;
+      }
+      return scale;
+    };
+    float2 sc0 = issue(0, box_entry(0));
+    float2 sc1 = issue(1, box_entry(1));
+    int entry = box_entry(2);
+
+    // Q^T fragments: query row g of each tile, dims 16t..16t+15
+    uint32_t qb[kB][4][2];
+    float qs[kB][2];  // of rows 2t and 2t + 1: what a logit is multiplied by
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      const int r = 8 * b + g;
+      uint4 u = make_uint4(0, 0, 0, 0), w = u;
+      if (r < it.rows) {
+        const int a = it.rg * R + r, tok = p.by_group.div(a);
+        const uint4* q = reinterpret_cast<const uint4*>(p.q + (it.s.row0 + tok) * p.q_ts +
+                                                        (it.hk * p.group + a - tok * p.group) * p.q_hs + 16 * t);
+        u = q[0];
+        w = q[1];
+      }
+      uint32_t v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+      float mine = kLog2Scale;
+      if (kE4m3) {
+        // the row's largest exponent; then every value times 2^-e, as fp16
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mx = max(mx, max((v[j] >> 7) & 0xffu, (v[j] >> 23) & 0xffu));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = mx == 0xff ? 0 : min(max(static_cast<int>(mx) - 127, -120), 120);  // an infinity or NaN stays one
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        mine = kLog2Scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = pack_f16x2(__uint_as_float(v[j] << 16) * f, __uint_as_float(v[j] & 0xffff0000u) * f);
+      }
+      qs[b][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
+      qs[b][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        qb[b][kk][0] = v[2 * kk];
+        qb[b][kk][1] = v[2 * kk + 1];
+      }
+    }
+
+    float o[kB][4][4];
+    float ref[kB][2], l[kB][2];
+#pragma unroll
+    for (int b = 0; b < kB; ++b) {
+      ref[b][0] = ref[b][1] = -INFINITY;
+      l[b][0] = l[b][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.f;
+    }
+    bool part = false, unset = true;
+    int lv_lo = 200, lv_hi = -200;
+
+    for (int st = 0; st < n_steps; ++st) {
+      const int j0 = step_key(st);
+      const uint32_t slot = used & 1;
+      // the scales of the groups of 16 keys
+      float ks[kG], lv[kG], vi[kG];
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        if (kE4m3) {
+          const int src = (16 * i) >> p.box_log2;
+          ks[i] = __shfl_sync(0xffffffffu, sc0.x, src);
+          const uint32_t v = __float_as_uint(__shfl_sync(0xffffffffu, sc0.y, src)) & 0x7f800000u;
+          const int e = static_cast<int>(v >> 23) - 127;
+          lv_lo = min(lv_lo, e);
+          lv_hi = max(lv_hi, e);
+          lv[i] = static_cast<float>(e);
+          vi[i] = __uint_as_float((254u << 23) - v);
+        } else {
+          ks[i] = vi[i] = 1.f;
+          lv[i] = 0.f;
+        }
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (used >> 1) & 1, &sm.abort, kv.err, p.wait_budget, SAF3R_ERR_TIMEOUT));
+      if (!ok) break;
+      const uint8_t* kb = sm.buf[warp][slot];
+      const uint8_t* vb = kb + kStepBytes / 2;
+      const bool whole = (j0 >= it.last.lo && j0 + kT <= it.first.hi) || j0 + kT <= it.first.sink;  // every row sees every key
+      part |= !whole;
+
+      // S^T: keys sigma(g), sigma(g + 8) of each group; query rows 2t, 2t + 1 of each tile
+      float s[kB][kG][4];
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b) s[b][i][0] = s[b][i][1] = s[b][i][2] = s[b][i][3] = 0.f;
+        const int r0 = 16 * i + sigma(g), r1 = r0 + 8;
+        if (kE4m3) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kb + r0 * 64 + ((t ^ ((r0 >> 1) & 3)) << 4));
+          const uint4 y = *reinterpret_cast<const uint4*>(kb + r1 * 64 + ((t ^ ((r1 >> 1) & 3)) << 4));
+          const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t a[4] = {f16_of_e4m3(wx[kk]), f16_of_e4m3(wy[kk]), f16_of_e4m3(wx[kk] >> 16), f16_of_e4m3(wy[kk] >> 16)};
+#pragma unroll
+            for (int b = 0; b < kB; ++b) mma_f16(s[b][i], a, qb[b][kk][0], qb[b][kk][1]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kb + r0 * 128 + (((2 * t + c) ^ (r0 & 7)) << 4));
+            const uint4 y = *reinterpret_cast<const uint4*>(kb + r1 * 128 + (((2 * t + c) ^ (r1 & 7)) << 4));
+            const uint32_t a[4] = {x.x, y.x, x.y, y.y}, a2[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+              mma_bf16(s[b][i], a, qb[b][2 * c][0], qb[b][2 * c][1]);
+              mma_bf16(s[b][i], a2, qb[b][2 * c + 1][0], qb[b][2 * c + 1][1]);
+            }
           }
         }
       }
-    }
-    auto in = [&](int j) { return j < ub && (j >= ua || j < ue); };
-    // loads: keys, then values
-    uint4 k[kTiles][kE4m3 ? 1 : 2];
+      // to logits in units of log2 (times the value scale)
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      const int off = 8 * (n & 1) + g;
+      for (int b = 0; b < kB; ++b)
 #pragma unroll
-      for (int c = 0; c < (kE4m3 ? 1 : 2); ++c) {
-        k[n][c] = make_uint4(0, 0, 0, 0);
-        if (base[n / 2] >= 0 && in(j0 + 16 * (n / 2) + off))
-          k[n][c] = load_stream<uint4>(kv.k + ((base[n / 2] + off) * kD + 16 * t + 8 * c) * (kE4m3 ? 1 : 2));
+        for (int i = 0; i < kG; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[b][i][c] = fmaf(s[b][i][c], qs[b][c & 1] * ks[i], lv[i]);
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int r = it.rg * R + min(8 * b + 2 * t + c, it.rows - 1);
+            const Span sp = span_of(p.win, it.s.len - it.s.n_new + p.by_group.div(r), it.s.len);
+#pragma unroll
+            for (int i = 0; i < kG; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int j = j0 + 16 * i + sigma(g) + 8 * h;
+                if (!((j >= sp.lo && j < sp.hi) || j < sp.sink)) s[b][i][2 * h + c] = -INFINITY;
+              }
+          }
       }
-    }
-    uint32_t v[kT / 16][4][kE4m3 ? 2 : 4];
+      // the reference moves on the first step, and where a logit is far above it
+      bool raise = unset;
 #pragma unroll
-    for (int i = 0; i < kT / 16; ++i)
+      for (int b = 0; b < kB; ++b) {
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int off = 2 * t + (c & 1) + 8 * (c >> 1);
-        const bool have = base[i] >= 0 && in(j0 + 16 * i + off);
-        const uint8_t* src = kv.v + ((base[i] + off) * kD + 8 * g) * (kE4m3 ? 1 : 2);
-        if (kE4m3) {
-          const uint2 x = have ? load_stream<uint2>(src) : make_uint2(0, 0);
-          v[i][c][0] = x.x;
-          v[i][c][1] = x.y;
-        } else {
-          const uint4 x = have ? load_stream<uint4>(src) : make_uint4(0, 0, 0, 0);
-          v[i][c][0] = x.x;
-          v[i][c][1] = x.y;
-          v[i][c][kE4m3 ? 0 : 2] = x.z;
-          v[i][c][kE4m3 ? 1 : 3] = x.w;
-        }
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < kG; ++i) mx[c] = max3f(mx[c], s[b][i][c], s[b][i][2 + c]);
+        raise |= mx[0] > ref[b][0] + kRaise || mx[1] > ref[b][1] + kRaise;
       }
-    // logits, in units of log2, times nothing yet but the scales
-    float s[kTiles][4];
+      if (__any_sync(0xffffffffu, raise)) {
+        unset = false;
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      if (kE4m3) {
-        const uint32_t w[4] = {k[n][0].x, k[n][0].y, k[n][0].z, k[n][0].w};
+        for (int b = 0; b < kB; ++b)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_f16(s[n], qa[kk], f16_of_e4m3(w[kk]), f16_of_e4m3(w[kk] >> 16));
-      } else {
-        const uint4 x = k[n][0], y = k[n][kE4m3 ? 0 : 1];
-        mma_bf16(s[n], qa[0], x.x, x.y);
-        mma_bf16(s[n], qa[1], x.z, x.w);
-        mma_bf16(s[n], qa[2], y.x, y.y);
-        mma_bf16(s[n], qa[3], y.z, y.w);
-      }
-      const float f0 = qs[0] * ks[n / 2], f1 = qs[1] * ks[n / 2];
-      s[n][0] = s[n][0] * f0 + lv[n / 2];
-      s[n][1] = s[n][1] * f0 + lv[n / 2];
-      s[n][2] = s[n][2] * f1 + lv[n / 2];
-      s[n][3] = s[n][3] * f1 + lv[n / 2];
-    }
-    if (!whole) {
+          for (int c = 0; c < 2; ++c) {
+            float mx = ref[b][c];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n)
+            for (int i = 0; i < kG; ++i) mx = max3f(mx, s[b][i][c], s[b][i][2 + c]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int j = j0 + 8 * n + 2 * t + c;
-          const bool have = base[n / 2] >= 0;
-          if (!(have && ((j >= sg.lo && j < sg.hi) || j < sg.sink))) s[n][c] = -INFINITY;
-          if (!(have && ((j >= sh.lo && j < sh.hi) || j < sh.sink))) s[n][2 + c] = -INFINITY;
-        }
-      if (kv.max_new > 1) {
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float f = mx == ref[b][c] ? 1.f : fast_exp2(ref[b][c] - mx);  // from -inf: 0
+            ref[b][c] = mx;
+            unset |= mx == -INFINITY;
+            l[b][c] *= f;
 #pragma unroll
-        for (int i = 0; i < kT / 16; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int w = 0; w < (kE4m3 ? 2 : 4); ++w) {
-              const uint32_t x = v[i][c][w];
-              if (kE4m3)
-                bad |= (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // a code of 0x7f
-              else
-                bad |= (((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;  // an exponent of ones
+            for (int i = 0; i < 4; ++i) {
+              o[b][i][c] *= f;
+              o[b][i][2 + c] *= f;
             }
+          }
+        unset = __any_sync(0xffffffffu, unset);
       }
-    }
+      // P^T fragments
+      uint32_t pb[kB][kG][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mx = -INFINITY;
+      for (int b = 0; b < kB; ++b) {
+        const float u0 = ref[b][0] == -INFINITY ? 0.f : ref[b][0], u1 = ref[b][1] == -INFINITY ? 0.f : ref[b][1];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[i], mx);
-      const float use = mn == -INFINITY ? 0.f : mn;
-      const float f = fast_exp2(m[i] - use);
-      m[i] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        const float a = fast_exp2(s[n][2 * i] - use), b = fast_exp2(s[n][2 * i + 1] - use);
-        sum += (a + b) * vi[n / 2];
-        s[n][2 * i] = a;
-        s[n][2 * i + 1] = b;
-      }
-      l[i] = l[i] * f + sum;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        o[n][2 * i] *= f;
-        o[n][2 * i + 1] *= f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kT / 16; ++i) {
-      uint32_t pa4[4];
-      if (kE4m3) {
-        pa4[0] = pack_f16x2(s[2 * i][0], s[2 * i][1]);
-        pa4[1] = pack_f16x2(s[2 * i][2], s[2 * i][3]);
-        pa4[2] = pack_f16x2(s[2 * i + 1][0], s[2 * i + 1][1]);
-        pa4[3] = pack_f16x2(s[2 * i + 1][2], s[2 * i + 1][3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = __byte_perm(v[i][0][h], v[i][1][h], 0x5140), b = __byte_perm(v[i][0][h], v[i][1][h], 0x7362);
-          const uint32_t c = __byte_perm(v[i][2][h], v[i][3][h], 0x5140), d = __byte_perm(v[i][2][h], v[i][3][h], 0x7362);
-          mma_f16(o[4 * h], pa4, f16_of_e4m3(a), f16_of_e4m3(c));
-          mma_f16(o[4 * h + 1], pa4, f16_of_e4m3(a >> 16), f16_of_e4m3(c >> 16));
-          mma_f16(o[4 * h + 2], pa4, f16_of_e4m3(b), f16_of_e4m3(d));
-          mma_f16(o[4 * h + 3], pa4, f16_of_e4m3(b >> 16), f16_of_e4m3(d >> 16));
-        }
-      } else {
-        pa4[0] = pack_bf16x2(s[2 * i][0], s[2 * i][1]);
-        pa4[1] = pack_bf16x2(s[2 * i][2], s[2 * i][3]);
-        pa4[2] = pack_bf16x2(s[2 * i + 1][0], s[2 * i + 1][1]);
-        pa4[3] = pack_bf16x2(s[2 * i + 1][2], s[2 * i + 1][3]);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int w = kE4m3 ? 0 : h;
-          mma_bf16(o[2 * h], pa4, __byte_perm(v[i][0][w], v[i][1][w], 0x5410), __byte_perm(v[i][2][w], v[i][3][w], 0x5410));
-          mma_bf16(o[2 * h + 1], pa4, __byte_perm(v[i][0][w], v[i][1][w], 0x7632), __byte_perm(v[i][2][w], v[i][3][w], 0x7632));
+        for (int i = 0; i < kG; ++i) {
+          const float e0 = fast_exp2(s[b][i][0] - u0), e1 = fast_exp2(s[b][i][1] - u1);
+          const float e2 = fast_exp2(s[b][i][2] - u0), e3 = fast_exp2(s[b][i][3] - u1);
+          l[b][0] = fmaf(e0 + e2, vi[i], l[b][0]);
+          l[b][1] = fmaf(e1 + e3, vi[i], l[b][1]);
+          pb[b][i][0] = transpose8(kE4m3 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1));
+          pb[b][i][1] = transpose8(kE4m3 ? pack_f16x2(e2, e3) : pack_bf16x2(e2, e3));
         }
       }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        // value rows of the keys 2t, 2t + 1, 2t + 8, 2t + 9 of the group's order
+        uint32_t v[4][kE4m3 ? 2 : 4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int r = 16 * i + sigma(2 * t + (c & 1)) + 8 * (c >> 1);
+          if (kE4m3) {
+            const uint2 x = *reinterpret_cast<const uint2*>(vb + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+            v[c][0] = x.x;
+            v[c][1] = x.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(vb + r * 128 + ((g ^ (r & 7)) << 4));
+            v[c][0] = x.x;
+            v[c][1] = x.y;
+            v[c][kE4m3 ? 0 : 2] = x.z;
+            v[c][kE4m3 ? 1 : 3] = x.w;
+          }
+          if (!whole && !seen(j0 + r)) {  // what no row sees need not be finite
+#pragma unroll
+            for (int w = 0; w < (kE4m3 ? 2 : 4); ++w) v[c][w] = 0u;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {  // dims 8g + 2m and 8g + 2m + 1
+          uint32_t a[4];
+          if (kE4m3) {
+            const uint32_t sel = (m & 1) ? 0x7362 : 0x5140;
+            const uint32_t x = __byte_perm(v[0][m >> 1], v[1][m >> 1], sel), y = __byte_perm(v[2][m >> 1], v[3][m >> 1], sel);
+            a[0] = f16_of_e4m3(x);
+            a[1] = f16_of_e4m3(x >> 16);
+            a[2] = f16_of_e4m3(y);
+            a[3] = f16_of_e4m3(y >> 16);
+          } else {
+            const int w = kE4m3 ? 0 : m;
+            a[0] = __byte_perm(v[0][w], v[1][w], 0x5410);
+            a[1] = __byte_perm(v[0][w], v[1][w], 0x7632);
+            a[2] = __byte_perm(v[2][w], v[3][w], 0x5410);
+            a[3] = __byte_perm(v[2][w], v[3][w], 0x7632);
+          }
+#pragma unroll
+          for (int b = 0; b < kB; ++b) {
+            if (kE4m3)
+              mma_f16(o[b][m], a, pb[b][i][0], pb[b][i][1]);
+            else
+              mma_bf16(o[b][m], a, pb[b][i][0], pb[b][i][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the buffer
+      ++used;
+      sc0 = sc1;
+      sc1 = issue(st + 2, entry);
+      entry = box_entry(st + 3);
     }
-  }
-  // merge the warps: the lane's columns of rows g and g + 8 are dims 16t + nt and 16t + 8 + nt
+    if (!ok) break;
+
+    const bool wild = kE4m3 && lv_hi - lv_lo > kWild;
+    const bool only = c0 == 0 && c1 == it.ch.total;
+    Slot* sl = nullptr;
+    if (!only) sl = slots(p, R) + 2LL * (warp * gridDim.x + blockIdx.x) + (c0 > 0 ? 0 : 1);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    const int r = g + 8 * i;
+    for (int b = 0; b < kB; ++b)
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      s_o[warp][r][16 * t + n] = o[n][2 * i];
-      s_o[warp][r][16 * t + 8 + n] = o[n][2 * i + 1];
-    }
-    if (t == 0) {
-      s_m[warp][r] = m[i];
-      s_l[warp][r] = l[i];
-    }
-  }
-  if (bad) s_bad = 1;
-  __syncthreads();
-  const bool only = ch.total <= cps;  // the item has this piece alone
-  if (only && s_bad) {
-    exact_item(p, it, warp, lane);
-    return;
-  }
-  const int r = threadIdx.x >> 3, col = (threadIdx.x & 7) * 8;
-  float mm = -INFINITY, ll = 0.f, acc[8];
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[b][c];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float x[8];
+        bool bad = false;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = fast_exp2(s_m[w][r] - (mm == -INFINITY ? 0.f : mm));
-    ll += s_l[w][r] * f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += s_o[w][r][col + i] * f;
+        for (int i = 0; i < 8; ++i) {
+          x[i] = o[b][i >> 1][c + 2 * (i & 1)] * inv;
+          bad |= !(fabsf(x[i]) <= 3.402823466e+38f);
+        }
+        const int row = 8 * b + 2 * t + c;
+        const bool live = row < it.rows;
+        if (only) {
+          const uint32_t todo = __ballot_sync(0xffffffffu, live && ((bad && part) || wild));
+          if (live && !(todo & (0x11111111u << t))) store8(p, it, row, R, 8 * g, x);
+          for (int q = 0; q < 4; ++q)
+            if (todo & (0x11111111u << q)) exact_item_row(p, it, 8 * b + 2 * q + c, R, lane);
+        } else if (live) {
+          float4* d = reinterpret_cast<float4*>(&sl->o[row][8 * g]);
+          d[0] = make_float4(x[0], x[1], x[2], x[3]);
+          d[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (g == 0) {
+            sl->w[row] = sum == 0.f ? -INFINITY : ref[b][c] + log2f(sum);
+            sl->flags[row] = (part ? 1 : 0) | (wild ? 2 : 0);
+          }
+        }
+      }
   }
-  if (only) {
-    if (r < it.rows) store_row(p, it, r, col, acc, ll == 0.f ? 0.f : 1.f / ll);
-    return;
-  }
-  uint8_t* piece = piece_at(p, static_cast<long long>(blockIdx.z) * gridDim.y + blockIdx.y, blockIdx.x);
-  float4* po = reinterpret_cast<float4*>(reinterpret_cast<float*>(piece) + r * kD + col);
-  po[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  po[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-  Stats* ps = reinterpret_cast<Stats*>(piece + kRows * kD * sizeof(float));
-  if (col == 0) {
-    ps->m[r] = mm;
-    ps->l[r] = ll;
-  }
-  if (threadIdx.x == 0) ps->bad = s_bad;
+  // copies that a wait gave up on land before the block exits
+  for (; used < issued; ++used) mbar_wait_drain(&full[used & 1], (used >> 1) & 1, kDrainBudget);
 }
 
-// Joins the pieces of one item, in their order.
+// Joins the parts of one item (block x: its kv head and row group, y: its sequence).  A warp takes a row: the parts'
+// weights first, then 2 columns a lane, in their order.
+template <int kB>
 __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const __grid_constant__ KvAttnParams p) {
-  __shared__ int s_scratch[2 * kWarps];
-  const KvView& kv = p.kv;
-  const int cps = chunks_per_piece(p, gridDim.x / kv.n_heads, s_scratch);
-  const Item it = item_of(p, blockIdx.x, blockIdx.y);
-  if (it.rows <= 0) return;
-  const int pos0 = it.s.len - it.s.n_new;
-  const Span sa = span_of(p.win, pos0 + p.by_group.div(it.r0), it.s.len);
-  const Span sz = span_of(p.win, pos0 + p.by_group.div(it.r0 + it.rows - 1), it.s.len);
-  const Chunks ch = chunks_of(runs_of(sa.lo, sz.hi, sz.sink));
-  if (ch.total <= cps) return;
-  const int n = (ch.total + cps - 1) / cps;
-  const uint8_t* base = piece_at(p, static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x, 0);
-  auto stats = [&](int s) { return reinterpret_cast<const Stats*>(base + s * kPieceBytes + kRows * kD * sizeof(float)); };
-  const int r = threadIdx.x >> 3, col = (threadIdx.x & 7) * 8;
-  float mm = -INFINITY;
-  bool bad = false;
-  for (int s = 0; s < n; ++s) {
-    mm = fmaxf(mm, stats(s)->m[r]);
-    bad |= stats(s)->bad != 0;
-  }
-  if (bad) {
-    exact_item(p, it, threadIdx.x >> 5, threadIdx.x & 31);
-    return;
-  }
-  if (r >= it.rows) return;
-  float ll = 0.f, acc[8];
+  constexpr int R = 8 * kB;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = gridDim.x / p.kv.n_heads, hk = blockIdx.x / groups, rg = blockIdx.x - hk * groups;
+  const SeqInfo s = seq_info(p.kv, blockIdx.y);
+  const int rows = min(R, s.n_new * p.group - rg * R);
+  if (rows <= 0) return;
+  const ItemRec rec = recs(p)[item_index(p, blockIdx.y, hk, rg, R)];
+  const Share sh = *reinterpret_cast<const Share*>(p.ws);
+  const int i0 = share_of(sh, rec.x0), i1 = share_of(sh, rec.x0 + rec.chunks - 1);
+  if (i0 == i1) return;  // one warp had the whole item
+  const Slot* base = slots(p, R);
+  for (int row = warp; row < rows; row += kWarps) {
+    float big = -INFINITY, sum = 0.f, a0 = 0.f, a1 = 0.f;
+    int flags = 0;
+    for (int i = i0 + lane; i <= i1; i += 32) big = fmaxf(big, base[2LL * i + (i == i0 ? 1 : 0)].w[row]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int s = 0; s < n; ++s) {
-    const float f = fast_exp2(stats(s)->m[r] - (mm == -INFINITY ? 0.f : mm));
-    ll += stats(s)->l[r] * f;
-    const float4* po = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base + s * kPieceBytes) + r * kD + col);
-    const float4 a = po[0], b = po[1];
-    acc[0] += a.x * f; acc[1] += a.y * f; acc[2] += a.z * f; acc[3] += a.w * f;
-    acc[4] += b.x * f; acc[5] += b.y * f; acc[6] += b.z * f; acc[7] += b.w * f;
+    for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+    const float use = big == -INFINITY ? 0.f : big;
+    for (int i = i0; i <= i1; i += 32) {
+      const int n = min(32, i1 - i + 1);
+      float w = 0.f;
+      if (lane < n) {
+        const Slot& sl = base[2LL * (i + lane) + (i + lane == i0 ? 1 : 0)];
+        w = fast_exp2(sl.w[row] - use);
+        flags |= sl.flags[row];
+      }
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float f = __shfl_sync(0xffffffffu, w, k);
+        const float2 x = reinterpret_cast<const float2*>(base[2LL * (i + k) + (i + k == i0 ? 1 : 0)].o[row])[lane];
+        sum += f;
+        a0 += f * x.x;
+        a1 += f * x.y;
+      }
+    }
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    a0 *= inv;
+    a1 *= inv;
+    const bool bad = !(fabsf(a0) <= 3.402823466e+38f && fabsf(a1) <= 3.402823466e+38f);
+    const int i = rg * R + row, tok = p.by_group.div(i), head = hk * p.group + i - tok * p.group;
+    if ((flags & 2) || ((flags & 1) && __any_sync(0xffffffffu, bad))) {
+      exact_row(p, blockIdx.y, s.len, s.row0 + tok, s.len - s.n_new + tok, head, lane, 0, kD);
+      continue;
+    }
+    const long long at = (s.row0 + tok) * p.out_ts + head * p.out_hs + 2 * lane;
+    if (p.out_fp32)
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(a0, a1);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) = pack_bf16x2(a0, a1);
   }
-  store_row(p, it, r, col, acc, ll == 0.f ? 0.f : 1.f / ll);
 }
 
-int row_groups(int max_new, int group) { return (max_new * group + kRows - 1) / kRows; }
-
-// Most pieces of one item: its keys by at least 256, and not so many that idle blocks cost time.
-int split_limit(const KvView& kv, const WindowMask& w, int groups) {
-  long long keys = static_cast<long long>(kv.max_pages) << kv.page_log2;
-  if (w.window > 0) {
-    const long long views = (static_cast<long long>(kv.max_new) + w.view - 2) / w.view + 1;  // of the new tokens
-    const long long seen = (views + (w.causal ? 1LL : 2LL) * w.window) * w.view + w.sink + 128;
-    keys = keys < seen ? keys : seen;
-  }
-  const long long items = static_cast<long long>(kv.n_seqs) * kv.n_heads * groups;
-  long long n = (keys + 255) / 256;
-  const long long cap = items > 0 ? (16384 + items - 1) / items : 1;
-  n = n < cap ? n : cap;
-  n = n < 512 ? n : 512;
-  return n < 1 ? 1 : static_cast<int>(n);
-}
+int tile_rows(int max_new, int group) { return static_cast<long long>(max_new) * group <= 8 ? 8 : 16; }
 
 }  // namespace
 
 bool decode_takes(int max_new, int group) { return static_cast<long long>(max_new) * group <= 64; }
 
-size_t decode_workspace_bytes(const KvView& kv, const WindowMask& w, int group) {
-  const int groups = row_groups(kv.max_new, group);
-  return static_cast<size_t>(kv.n_seqs) * kv.n_heads * groups * split_limit(kv, w, groups) * kPieceBytes;
+size_t decode_workspace_bytes(const KvView& kv, int group) {
+  const int R = tile_rows(kv.max_new, group);
+  const size_t items = static_cast<size_t>(kv.n_seqs) * kv.n_heads * ((static_cast<size_t>(kv.max_new) * group + R - 1) / R);
+  return sizeof(Share) * 16 + items * sizeof(ItemRec) + kMaxShares * 2 * sizeof(Slot);
 }
 
-cudaError_t launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_launch) {
+saf3r_status launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_launch) {
   KvAttnParams p = p0;
-  const int groups = row_groups(p.kv.max_new, p.group);
-  p.n_split = split_limit(p.kv, p.win, groups);
-  const dim3 grid(p.n_split, p.kv.n_heads * groups, p.kv.n_seqs);
-  if (p.e4m3)
-    decode_kernel<true><<<grid, 32 * kWarps, 0, stream>>>(p);
-  else
-    decode_kernel<false><<<grid, 32 * kWarps, 0, stream>>>(p);
+  const KvView& kv = p.kv;
+  const int keys = p.e4m3 ? 64 : 32, box = kv.page < keys ? kv.page : keys;
+  p.box_log2 = box == 16 ? 4 : box == 32 ? 5 : 6;
+  p.least_share = p.e4m3 ? 4 : 2;
+  const long long rows = static_cast<long long>(kv.n_pages) * kv.n_heads * kv.page;
+  CUtensorMap mk, mv;
+  if (!(p.e4m3 ? make_map_codes(&mk, kv.k, rows, box, true) && make_map_codes(&mv, kv.v, rows, box, true)
+               : make_map_rows(&mk, kv.k, rows, kD, 1, rows * kD, box) && make_map_rows(&mv, kv.v, rows, kD, 1, rows * kD, box)))
+    return SAF3R_ERR_CUDA;
+  const bool wide = tile_rows(kv.max_new, p.group) == 16;
+  const auto kernel = p.e4m3 ? (wide ? decode_kernel<true, 2> : decode_kernel<true, 1>) : (wide ? decode_kernel<false, 2> : decode_kernel<false, 1>);
+  const int smem = static_cast<int>(sizeof(DecodeSmem) + 1024);
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SAF3R_ERR_CUDA;
+  const int grid = (p.num_sms < 160 ? p.num_sms : 160) * kBlocksPerSm;
+  kernel<<<grid, 32 * kWarps, smem, stream>>>(p, mk, mv);
   ++*n_launch;
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.n_split == 1) return e;
-  decode_join_kernel<<<dim3(grid.y, grid.z), 32 * kWarps, 0, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
+  // the join's blocks are set up while the first kernel still runs, and wait for its end on the device
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  const int R = wide ? 16 : 8;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kv.n_heads * ((kv.max_new * p.group + R - 1) / R), kv.n_seqs);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, wide ? decode_join_kernel<2> : decode_join_kernel<1>, p) != cudaSuccess) return SAF3R_ERR_CUDA;
   ++*n_launch;
-  return cudaGetLastError();
+  return SAF3R_OK;
 }
 
 }  // namespace saf3r

@@ -97,8 +97,8 @@ struct KvAttnParams {
   int32_t num_sms;
   long long wait_budget;
   int32_t withhold;
-  int32_t n_split;     // decode: most pieces of one item
-  int32_t box_log2;    // tensor cores: keys of one TMA box (a page, at most 64)
+  int32_t least_share; // few rows: chunks that are worth a warp
+  int32_t box_log2;    // keys of one TMA box
 };
 
 #ifdef __CUDACC__
@@ -178,8 +178,8 @@ cudaError_t launch_append(const AppendParams& p, bool e4m3, int num_sms, cudaStr
 
 // few query rows per sequence and kv head (kv_decode.cu)
 bool decode_takes(int max_new, int group);
-size_t decode_workspace_bytes(const KvView& kv, const WindowMask& w, int group);
-cudaError_t launch_decode(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
+size_t decode_workspace_bytes(const KvView& kv, int group);
+saf3r_status launch_decode(const KvAttnParams& p, cudaStream_t stream, int* n_launch);
 
 // the tensor-core kernel (kv_attn_sm100.cu)
 size_t attn_workspace_bytes();
@@ -193,6 +193,6 @@ long long call_wait_budget();
 bool take_withhold_arrive();
 bool make_map_rows(CUtensorMap* m, const void* base, long long rows, long long row_stride, int heads,
                    long long head_stride, int box_rows);
-bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows);
+bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows, bool swizzle);
 
 }  // namespace saf3r

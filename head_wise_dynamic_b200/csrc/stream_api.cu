@@ -174,7 +174,7 @@ size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv
   const KvView kv = view_of(cache, batch, nullptr);
   const int group = n_heads / cache->n_heads;
   const size_t n = decode_takes(batch->max_new, group)
-                       ? decode_workspace_bytes(kv, mask_of(window), group)
+                       ? decode_workspace_bytes(kv, group)
                        : attn_workspace_bytes();
   return n < 256 ? 256 : n;
 }
@@ -216,7 +216,7 @@ saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* ba
   p.wait_budget = call_wait_budget();
   int launches = 0;
   if (decode_takes(batch->max_new, p.group))
-    st = cuda_status(launch_decode(p, static_cast<cudaStream_t>(stream), &launches));
+    st = launch_decode(p, static_cast<cudaStream_t>(stream), &launches);
   else {
     p.withhold = take_withhold_arrive();
     st = launch_attn(p, static_cast<cudaStream_t>(stream), &launches);
