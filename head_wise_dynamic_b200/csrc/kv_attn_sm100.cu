@@ -54,7 +54,7 @@ constexpr int kMaxShares = 160;        // CTAs of a launch at most (one for each
 constexpr int kPlanEntries = 1024;
 // Cost of a key block and of an item's start and end, in sixteenths of a two-tile block.
 constexpr int kCost2 = 16, kCost1 = 13, kCostItem = 16;
-constexpr int kLeastShare = 4 * kCost2;  // shares smaller than this are not worth a CTA
+constexpr int kLeastShare = 2 * kCost2;  // shares smaller than this are not worth a CTA
 
 // Pairs (of the 32 of a row's 64 keys) whose exponentials run on the FMA pipe.
 constexpr uint32_t kPolyPairs = 0x80808080u;
@@ -1115,6 +1115,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // registers: launched with 96 x 640 or 80 x 768; 64 x 128 + 104 x 512 and 64 x 256 + 88 x 512 are as many
   if (warp < Ring<kE4m3>::kSoftmax) {
@@ -1158,6 +1159,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
 // Finishes the items that shares' borders cut: block (i, y) has rows 32y.. of the item first cut by share i's
 // start.  8 threads a row, 8 columns each; pieces in their order.
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Work& wk = *reinterpret_cast<const Work*>(p.ws);
   const Cut& cut = wk.cuts[blockIdx.x + 1];
   const int r = blockIdx.y * 32 + (threadIdx.x >> 3), col = (threadIdx.x & 7) * 8, lane = threadIdx.x & 31;
@@ -1245,9 +1247,18 @@ saf3r_status launch_attn(const KvAttnParams& p0, cudaStream_t stream, int* n_lau
   ++*n_launch;
   if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
   if (grid > 1) {
-    kv_join_kernel<<<dim3(grid - 1, kItem / 32), 256, 0, stream>>>(p);
+    // its blocks are set up while the first kernel still runs, and wait for its end on the device
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid - 1, kItem / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kv_join_kernel, p) != cudaSuccess) return SAF3R_ERR_CUDA;
     ++*n_launch;
-    if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
   }
   return SAF3R_OK;
 }

@@ -70,21 +70,10 @@ struct Slot {
   float w[kMaxRows];
   int32_t flags[kMaxRows];  // 1: some streamed key is out of the row's sight, 2: value scales too far apart
 };
-// Where an item lies on the line of all chunks (written by the warp that begins it).
+// The shares that hold an item's first and last chunk (written by those warps).
 struct ItemRec {
-  long long x0;
-  int32_t chunks, pad;
+  int32_t first, last;
 };
-
-struct Share {
-  long long each;
-  int32_t extra, shares;
-};
-__device__ __forceinline__ long long share_start(const Share& sh, int i) { return sh.each * i + min(i, sh.extra); }
-__device__ __forceinline__ int share_of(const Share& sh, long long x) {
-  const long long big = (sh.each + 1) * sh.extra;
-  return static_cast<int>(x < big ? x / (sh.each + 1) : sh.extra + (x - big) / sh.each);
-}
 
 // Row group rg of a sequence: rows rg * R.. of its (token, group head) rows.
 struct Item {
@@ -122,11 +111,8 @@ __device__ __forceinline__ long long item_index(const KvAttnParams& p, int b, in
   const int groups = (p.kv.max_new * p.group + R - 1) / R;
   return (static_cast<long long>(b) * p.kv.n_heads + hk) * groups + rg;
 }
-__device__ __forceinline__ ItemRec* recs(const KvAttnParams& p) { return reinterpret_cast<ItemRec*>(p.ws + sizeof(Share) * 16); }
-__device__ __forceinline__ Slot* slots(const KvAttnParams& p, int R) {
-  const long long items = item_index(p, p.kv.n_seqs, 0, 0, R);
-  return reinterpret_cast<Slot*>(p.ws + sizeof(Share) * 16 + items * sizeof(ItemRec));
-}
+__device__ __forceinline__ Slot* slots(const KvAttnParams& p) { return reinterpret_cast<Slot*>(p.ws); }
+__device__ __forceinline__ ItemRec* recs(const KvAttnParams& p) { return reinterpret_cast<ItemRec*>(p.ws + kMaxShares * 2 * sizeof(Slot)); }
 
 // Walks the pieces of a warp's share.
 struct Walk {
@@ -135,7 +121,7 @@ struct Walk {
   SeqInfo s;
 
   // the next piece: chunks c0 .. c1 - 1 of the item
-  __device__ __forceinline__ bool next(const KvAttnParams& p, int R, Item& it, int& c0, int& c1, long long& x0) {
+  __device__ __forceinline__ bool next(const KvAttnParams& p, int R, Item& it, int& c0, int& c1) {
     while (x < xe) {
       while (rg >= row_groups(p, s, R)) {
         rg = 0;
@@ -146,7 +132,6 @@ struct Walk {
         }
       }
       it = item_of(p, s, b, hk, rg, R);
-      x0 = x;
       const long long d0 = xs - x, d1 = xe - x;
       c0 = d0 <= 0 ? 0 : (d0 < it.ch.total ? static_cast<int>(d0) : it.ch.total);
       c1 = d1 < it.ch.total ? static_cast<int>(d1) : it.ch.total;
@@ -159,7 +144,7 @@ struct Walk {
 };
 
 // Finds every warp's share (run by the whole block; each warp gets its own walk).
-__device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long long* entries, Share& sh) {
+__device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long long* entries) {
   constexpr int kThreads = 32 * kWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.kv.n_seqs;
   const int per = (n + kThreads - 1) / kThreads;
@@ -178,17 +163,18 @@ __device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long lon
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += entries[32 * w + 31];
   const int most = gridDim.x * kWarps;
-  sh.shares = total >= static_cast<long long>(most) * p.least_share ? most : max(1, static_cast<int>(total) / p.least_share);
-  sh.each = total / sh.shares;
-  sh.extra = static_cast<int>(total - sh.each * sh.shares);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<Share*>(p.ws) = sh;
+  const int shares = total >= static_cast<long long>(most) * p.least_share ? most : max(1, static_cast<int>(total) / p.least_share);
+  // (a 64-bit division takes several times as long)
+  const long long each = total >> 31 ? total / shares : static_cast<long long>(static_cast<uint32_t>(total) / static_cast<uint32_t>(shares));
+  const int extra = static_cast<int>(total - each * shares);
+  auto share_start = [&](int i) { return each * i + min(i, extra); };
   // neighbouring shares go to different SMs: few streams spread over all of them
   const int me = warp * gridDim.x + blockIdx.x;
   Walk w;
   w.b = w.hk = w.rg = 0;
   w.s = SeqInfo{0, 0, 0, false};
-  w.xs = me < sh.shares ? share_start(sh, me) : total;
-  w.xe = me < sh.shares ? share_start(sh, me + 1) : total;
+  w.xs = me < shares ? share_start(me) : total;
+  w.xe = me < shares ? share_start(me + 1) : total;
   w.x = w.xs;
   if (w.xs >= w.xe) return w;
   long long rest = w.xs;
@@ -272,8 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
     sm.abort = 0;
     fence_mbar_init();
   }
-  Share sh;
-  Walk walk = make_walk(p, R, sm.entries, sh);  // (syncs the block)
+  Walk walk = make_walk(p, R, sm.entries);  // (syncs the block)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   uint64_t* full = sm.full[warp];
@@ -283,9 +268,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
   auto sigma = [](int m) { return m ^ ((m >> 1) & 1); };
   Item it;
   int c0, c1;
-  long long x0;
-  while (ok && walk.next(p, R, it, c0, c1, x0)) {
-    if (c0 == 0 && lane == 0) recs(p)[item_index(p, it.b, it.hk, it.rg, R)] = ItemRec{x0, it.ch.total, 0};
+  const int me = warp * gridDim.x + blockIdx.x;
+  while (ok && walk.next(p, R, it, c0, c1)) {
+    if (lane == 0) {
+      ItemRec* rec = recs(p) + item_index(p, it.b, it.hk, it.rg, R);
+      if (c0 == 0) rec->first = me;
+      if (c1 == it.ch.total) rec->last = me;
+    }
     const int n_steps = (c1 - c0) * kSteps;
     const int32_t* table = kv.table + static_cast<long long>(it.b) * kv.max_pages;
     auto step_key = [&](int i) { return it.ch.key(c0 + i / kSteps) + (i % kSteps) * kT; };
@@ -577,7 +566,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
     const bool wild = kE4m3 && lv_hi - lv_lo > kWild;
     const bool only = c0 == 0 && c1 == it.ch.total;
     Slot* sl = nullptr;
-    if (!only) sl = slots(p, R) + 2LL * (warp * gridDim.x + blockIdx.x) + (c0 > 0 ? 0 : 1);
+    if (!only) sl = slots(p) + 2LL * me + (c0 > 0 ? 0 : 1);
 #pragma unroll
     for (int b = 0; b < kB; ++b)
 #pragma unroll
@@ -615,47 +604,80 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
   for (; used < issued; ++used) mbar_wait_drain(&full[used & 1], (used >> 1) & 1, kDrainBudget);
 }
 
-// Joins the parts of one item (block x: its kv head and row group, y: its sequence).  A warp takes a row: the parts'
-// weights first, then 2 columns a lane, in their order.
+// Joins the parts of one item (block x: its kv head and row group, y: its sequence).  Few rows get several warps each, which
+// take parts in turn: their weights first, then 2 columns a lane, in a fixed order.
+constexpr int kJoinWarps = 8;
 template <int kB>
-__global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __grid_constant__ KvAttnParams p) {
   constexpr int R = 8 * kB;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float s_a[kJoinWarps][kD], s_big[kJoinWarps], s_sum[kJoinWarps];
+  __shared__ int s_flags[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = gridDim.x / p.kv.n_heads, hk = blockIdx.x / groups, rg = blockIdx.x - hk * groups;
-  const SeqInfo s = seq_info(p.kv, blockIdx.y);
+  const SeqInfo s = seq_info(p.kv, blockIdx.y);  // the call's input: the first kernel does not write it
   const int rows = min(R, s.n_new * p.group - rg * R);
   if (rows <= 0) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const ItemRec rec = recs(p)[item_index(p, blockIdx.y, hk, rg, R)];
-  const Share sh = *reinterpret_cast<const Share*>(p.ws);
-  const int i0 = share_of(sh, rec.x0), i1 = share_of(sh, rec.x0 + rec.chunks - 1);
+  const int i0 = rec.first, i1 = rec.last;
   if (i0 == i1) return;  // one warp had the whole item
-  const Slot* base = slots(p, R);
-  for (int row = warp; row < rows; row += kWarps) {
+  const int turn = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;  // warps of a row
+  const int at0 = warp & (turn - 1);
+  const Slot* base = slots(p);
+  auto slot = [&](int i) -> const Slot& { return base[2LL * i + (i == i0 ? 1 : 0)]; };
+  for (int row = warp / turn; row < rows; row += kJoinWarps / turn) {
     float big = -INFINITY, sum = 0.f, a0 = 0.f, a1 = 0.f;
     int flags = 0;
-    for (int i = i0 + lane; i <= i1; i += 32) big = fmaxf(big, base[2LL * i + (i == i0 ? 1 : 0)].w[row]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-    const float use = big == -INFINITY ? 0.f : big;
-    for (int i = i0; i <= i1; i += 32) {
-      const int n = min(32, i1 - i + 1);
-      float w = 0.f;
-      if (lane < n) {
-        const Slot& sl = base[2LL * (i + lane) + (i + lane == i0 ? 1 : 0)];
-        w = fast_exp2(sl.w[row] - use);
-        flags |= sl.flags[row];
+    for (int i = i0 + at0; i <= i1; i += 32 * turn) {  // 32 parts at a time
+      float w = -INFINITY;
+      const int mine = i + lane * turn;
+      if (mine <= i1) {
+        w = slot(mine).w[row];
+        flags |= slot(mine).flags[row];
       }
+      float now = w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+      now = fmaxf(now, big);
+      const float f = big == now ? 1.f : fast_exp2(big - now);  // from -inf: 0
+      big = now;
+      sum *= f;
+      a0 *= f;
+      a1 *= f;
+      w = w == -INFINITY ? 0.f : fast_exp2(w - big);
+      const int n = min(32, (i1 - i) / turn + 1);
 #pragma unroll 8
       for (int k = 0; k < n; ++k) {
-        const float f = __shfl_sync(0xffffffffu, w, k);
-        const float2 x = reinterpret_cast<const float2*>(base[2LL * (i + k) + (i + k == i0 ? 1 : 0)].o[row])[lane];
-        sum += f;
-        a0 += f * x.x;
-        a1 += f * x.y;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float2 x = reinterpret_cast<const float2*>(slot(i + k * turn).o[row])[lane];
+        sum += wk;
+        a0 += wk * x.x;
+        a1 += wk * x.y;
       }
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
+    if (turn > 1) {  // every warp of the block has one row then
+      s_a[warp][2 * lane] = a0;
+      s_a[warp][2 * lane + 1] = a1;
+      if (lane == 0) {
+        s_big[warp] = big;
+        s_sum[warp] = sum;
+        s_flags[warp] = flags;
+      }
+    }
+    if (turn > 1) {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / turn), "r"(32 * turn) : "memory");  // the row's warps
+      if (at0 > 0) return;
+      for (int q = 1; q < turn; ++q) big = fmaxf(big, s_big[warp + q]);
+      sum = a0 = a1 = 0.f;
+      for (int q = 0; q < turn; ++q) {
+        const float f = s_big[warp + q] == -INFINITY ? 0.f : fast_exp2(s_big[warp + q] - big);
+        sum += f * s_sum[warp + q];
+        a0 += f * s_a[warp + q][2 * lane];
+        a1 += f * s_a[warp + q][2 * lane + 1];
+        flags |= s_flags[warp + q];
+      }
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     a0 *= inv;
     a1 *= inv;
@@ -682,7 +704,7 @@ bool decode_takes(int max_new, int group) { return static_cast<long long>(max_ne
 size_t decode_workspace_bytes(const KvView& kv, int group) {
   const int R = tile_rows(kv.max_new, group);
   const size_t items = static_cast<size_t>(kv.n_seqs) * kv.n_heads * ((static_cast<size_t>(kv.max_new) * group + R - 1) / R);
-  return sizeof(Share) * 16 + items * sizeof(ItemRec) + kMaxShares * 2 * sizeof(Slot);
+  return kMaxShares * 2 * sizeof(Slot) + items * sizeof(ItemRec);
 }
 
 saf3r_status launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_launch) {
@@ -690,7 +712,7 @@ saf3r_status launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_l
   const KvView& kv = p.kv;
   const int keys = p.e4m3 ? 64 : 32, box = kv.page < keys ? kv.page : keys;
   p.box_log2 = box == 16 ? 4 : box == 32 ? 5 : 6;
-  p.least_share = p.e4m3 ? 4 : 2;
+  p.least_share = p.e4m3 ? 2 : 1;  // two steps: both of a warp's buffers
   const long long rows = static_cast<long long>(kv.n_pages) * kv.n_heads * kv.page;
   CUtensorMap mk, mv;
   if (!(p.e4m3 ? make_map_codes(&mk, kv.k, rows, box, true) && make_map_codes(&mv, kv.v, rows, box, true)
@@ -711,7 +733,7 @@ saf3r_status launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_l
   const int R = wide ? 16 : 8;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kv.n_heads * ((kv.max_new * p.group + R - 1) / R), kv.n_seqs);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
