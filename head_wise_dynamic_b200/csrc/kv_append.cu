@@ -10,6 +10,7 @@
 //
 // Scales are powers of two: x / scale is exact, and re-rounding older codes when a scale grows is too
 // unless they become subnormal.
+#include "rope.cuh"
 #include "stream.h"
 
 namespace saf3r {
@@ -30,34 +31,29 @@ struct Chunk {
 __device__ __forceinline__ Chunk find_chunk(const KvView& kv, int x, int lane) {
   int b = -1, idx = 0;  // sequence, page of its new rows
   SeqInfo s{0, 0, 0, false};
-  if (kv.max_new == 1) {
-    b = x;
-    s = seq_info(kv, b);
-  } else {
-    int before = 0;
-    for (int b0 = 0; b0 < kv.n_seqs && b < 0; b0 += 32) {
-      SeqInfo mine{0, 0, 0, false};
-      if (b0 + lane < kv.n_seqs) mine = seq_info(kv, b0 + lane);
-      int cnt = 0;
-      if (mine.n_new > 0)
-        cnt = ((mine.len - 1) >> kv.page_log2) - ((mine.len - mine.n_new) >> kv.page_log2) + 1;
-      int incl = cnt;
+  int before = 0;
+  for (int b0 = 0; b0 < kv.n_seqs && b < 0; b0 += 32) {
+    SeqInfo mine{0, 0, 0, false};
+    if (b0 + lane < kv.n_seqs) mine = seq_info(kv, b0 + lane);
+    int cnt = 0;
+    if (mine.n_new > 0)
+      cnt = ((mine.len - 1) >> kv.page_log2) - ((mine.len - mine.n_new) >> kv.page_log2) + 1;
+    int incl = cnt;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, cnt > 0 && x >= before + incl - cnt && x < before + incl);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b = b0 + src;
-        idx = x - before - __shfl_sync(0xffffffffu, incl - cnt, src);
-        s.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
-        s.n_new = __shfl_sync(0xffffffffu, mine.n_new, src);
-        s.len = __shfl_sync(0xffffffffu, mine.len, src);
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
     }
+    const uint32_t hit = __ballot_sync(0xffffffffu, cnt > 0 && x >= before + incl - cnt && x < before + incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = b0 + src;
+      idx = x - before - __shfl_sync(0xffffffffu, incl - cnt, src);
+      s.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
+      s.n_new = __shfl_sync(0xffffffffu, mine.n_new, src);
+      s.len = __shfl_sync(0xffffffffu, mine.len, src);
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
   }
   Chunk c{-1, 0, 0, 0};
   if (b < 0 || s.n_new <= 0) return c;
@@ -76,15 +72,6 @@ __device__ __forceinline__ Chunk find_chunk(const KvView& kv, int x, int lane) {
   return c;
 }
 
-__device__ __forceinline__ void unpack(uint2 x, float (&v)[8], int at) {
-  v[at] = __uint_as_float(x.x << 16); v[at + 1] = __uint_as_float(x.x & 0xffff0000u);
-  v[at + 2] = __uint_as_float(x.y << 16); v[at + 3] = __uint_as_float(x.y & 0xffff0000u);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
@@ -115,8 +102,76 @@ __device__ __forceinline__ int scale_exp(float m) {
   return min(max(e - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0), kMinExp), kMaxExp);
 }
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ AppendParams p) {
+// Old codes of a page's first `rows` rows, rounded again to a larger scale (f = old scale / new one); `threads` threads.
+__device__ __forceinline__ void rescale_rows(uint8_t* rows_at, int rows, float f, int thread, int threads) {
+  uint4* old = reinterpret_cast<uint4*>(rows_at);
+  const int n = rows * 4;
+  for (int i0 = thread; i0 < n; i0 += 4 * threads) {  // four loads at a time
+    uint4 v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (i0 + c * threads < n) v[c] = old[i0 + c * threads];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (i0 + c * threads < n)
+        old[i0 + c * threads] = make_uint4(rescale4(v[c].x, f), rescale4(v[c].y, f), rescale4(v[c].z, f), rescale4(v[c].w, f));
+  }
+}
+
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// a segment's codes at p (its 4 or 8 bytes)
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, float (&x)[N], float inv) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = fabsf(x[i]) <= kFltMax ? x[i] * inv : __uint_as_float(0x7fffffffu);
+  if constexpr (N == 4) {
+    *reinterpret_cast<uint32_t*>(p) = e4m3x4(x[0], x[1], x[2], x[3]);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+  }
+}
+template <int N>
+__device__ __forceinline__ float largest(const float (&x)[N], float m) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float a = fabsf(x[i]);
+    m = fmaxf(m, a <= kFltMax ? a : 0.f);  // infinities and NaN do not count
+  }
+  return m;
+}
+template <int N>
+__device__ __forceinline__ void store_rows(uint16_t* row, int o1, int o2, const float (&a)[N], const float (&b)[N]) {
+  Segment<uint16_t, N> u, w;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    u.set2(i, a[i], a[i + 1]);
+    w.set2(i, b[i], b[i + 1]);
+  }
+  u.store(row + o1);
+  w.store(row + o2);
+}
+
+// Dims of a thread's two segments: those of the rotation, or 2 kSeg neighbours.
+template <int kSeg>
+__device__ __forceinline__ void segments(const RopeTable& tb, bool rope, int g, int& o1, int& o2) {
+  o1 = 2 * kSeg * g;
+  o2 = o1 + kSeg;
+  if (rope) {
+    o1 = kSeg == 8 ? tb.wide1[g] : tb.o1[g];
+    o2 = kSeg == 8 ? tb.wide2[g] : tb.o2[g];
+  }
+}
+
+// A thread's rows of one task as they come from memory.
+template <int kSeg>
+struct RawRows {
+  Segment<uint16_t, kSeg> u[16 / kSeg], w[16 / kSeg];
+};
+
+template <bool kE4m3, int kSeg>
+__global__ void __launch_bounds__(32 * kWarps, 3) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = 32 / kSeg, kSteps = 16 / kSeg;  // threads of a row; rows of a step are kSeg
   __shared__ Chunk s_chunk;
   __shared__ float s_amax[2][kWarps];
   extern __shared__ float2 s_sc[];  // [rows of the page][32] (sine, cosine), with a rope
@@ -130,6 +185,30 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   const Chunk c = s_chunk;
   if (c.page < 0) return;
   const RopeTable& tb = p.rope;
+  const int team_warps = kv.page >> 4, teams = kWarps / team_warps;
+  const int team = warp / team_warps, wt = warp - team * team_warps;
+  const int h0 = blockIdx.y * p.heads_per_block;
+  const int tasks = 2 * (min(h0 + p.heads_per_block, kv.n_heads) - h0);  // a head's keys, its values, the next head's keys, ..
+  const int g = lane % kLanes, r0 = wt * 16 + lane / kLanes - c.row0;    // rows r0, r0 + kSeg, .. of the new ones
+  auto load = [&](int task, RawRows<kSeg>& x) {
+    if (task >= tasks) return;
+    const bool is_k = (task & 1) == 0;
+    int o1, o2;
+    segments<kSeg>(tb, is_k && p.has_rope, g, o1, o2);
+    const int head = h0 + (task >> 1);
+    const uint16_t* src = is_k ? p.k_rows + head * p.k_hs : p.v_rows + head * p.v_hs;
+    const long long ts = is_k ? p.k_ts : p.v_ts;
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      const int r = r0 + st * kSeg;
+      if (r < 0 || r >= c.n) continue;
+      const uint16_t* row = src + (c.token + r) * ts;
+      x.u[st].load(row + o1);
+      x.w[st].load(row + o2);
+    }
+  };
+  RawRows<kSeg> now, next;
+  load(team, now);  // on their way while the angles are worked out
   if (p.has_rope) {
     const int np = 4 * tb.n_groups;
     for (int i = threadIdx.x; i < c.n * 32; i += 32 * kWarps) {
@@ -143,125 +222,170 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
     }
     __syncthreads();
   }
-  const int team_warps = kv.page >> 4, teams = kWarps / team_warps;
-  const int team = warp / team_warps, wt = warp - team * team_warps;
-  const int h0 = blockIdx.y * p.heads_per_block;
-  const int tasks = 2 * (min(h0 + p.heads_per_block, kv.n_heads) - h0);
-  const int g = lane & 7;
   for (int i0 = 0, par = 0; i0 < tasks; i0 += teams, par ^= 1) {
     const int task = i0 + team;
     const bool live = task < tasks;
     const int head = h0 + (task >> 1);
     const bool is_k = (task & 1) == 0;
-    const bool turns = is_k && p.has_rope && g < tb.n_groups;
-    const int o1 = is_k && p.has_rope ? tb.o1[g] : 8 * g;
-    const int o2 = is_k && p.has_rope ? tb.o2[g] : 8 * g + 4;
-    const uint16_t* src = (is_k ? p.k_rows : p.v_rows) + head * (is_k ? p.k_hs : p.v_hs);
-    const long long ts = is_k ? p.k_ts : p.v_ts;
+    const bool turns = is_k && p.has_rope && g * kSeg < 4 * tb.n_groups;
+    int o1, o2;
+    segments<kSeg>(tb, is_k && p.has_rope, g, o1, o2);
     const long long block = (static_cast<long long>(c.page) * kv.n_heads + head) << kv.page_log2;  // first row
-    float x[4][8];
-    uint2 raw[4][2];
-    bool in[4];
+    load(task + teams, next);
+    // step st's values, turned (8-bit: twice, once for the largest and once to store; it costs less than keeping them)
+    auto values = [&](int st, float(&a)[kSeg], float(&b)[kSeg]) {
+      spread(now.u[st], now.w[st], a, b);
+      if (!turns) return;
+      const float4* sc = reinterpret_cast<const float4*>(s_sc + (r0 + st * kSeg) * 32 + kSeg * g);
+      float s[kSeg], co[kSeg];
 #pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      const int r = wt * 16 + st * 4 + (lane >> 3) - c.row0;
-      in[st] = live && r >= 0 && r < c.n;
-      if (in[st]) {
-        const uint16_t* row = src + (c.token + r) * ts;
-        raw[st][0] = *reinterpret_cast<const uint2*>(row + o1);
-        raw[st][1] = *reinterpret_cast<const uint2*>(row + o2);
+      for (int i = 0; i < kSeg / 2; ++i) {
+        const float4 x = sc[i];
+        s[2 * i] = x.x; co[2 * i] = x.y; s[2 * i + 1] = x.z; co[2 * i + 1] = x.w;
       }
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      if (!in[st]) continue;
-      unpack(raw[st][0], x[st], 0);
-      unpack(raw[st][1], x[st], 4);
-      if (turns) {
-        const int r = wt * 16 + st * 4 + (lane >> 3) - c.row0;
-        const float4* sc = reinterpret_cast<const float4*>(s_sc + r * 32 + 4 * g);
-        const float4 t0 = sc[0], t1 = sc[1];
-        const float s[4] = {t0.x, t0.z, t1.x, t1.z}, co[4] = {t0.y, t0.w, t1.y, t1.w};
-        if (tb.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[st][2 * i], b = x[st][2 * i + 1];
-            x[st][2 * i] = a * co[i] - b * s[i];
-            x[st][2 * i + 1] = a * s[i] + b * co[i];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[st][i], b = x[st][4 + i];
-            x[st][i] = a * co[i] - b * s[i];
-            x[st][4 + i] = a * s[i] + b * co[i];
-          }
-        }
-      }
-      if (kE4m3) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = fabsf(x[st][i]);
-          amax = fmaxf(amax, a <= kFltMax ? a : 0.f);  // infinities and NaN do not count
-        }
-      }
-    }
+      turn(a, b, s, co, tb.interleaved);
+    };
+    auto in = [&](int st) { return live && r0 + st * kSeg >= 0 && r0 + st * kSeg < c.n; };
     if constexpr (!kE4m3) {
-      uint16_t* dst = reinterpret_cast<uint16_t*>(is_k ? kv.k : kv.v) + block * kD;
 #pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        if (!in[st]) continue;
-        uint16_t* row = dst + (wt * 16 + st * 4 + (lane >> 3)) * kD;
-        *reinterpret_cast<uint2*>(row + o1) = make_uint2(pack2(x[st][0], x[st][1]), pack2(x[st][2], x[st][3]));
-        *reinterpret_cast<uint2*>(row + o2) = make_uint2(pack2(x[st][4], x[st][5]), pack2(x[st][6], x[st][7]));
+      for (int st = 0; st < kSteps; ++st) {
+        if (!in(st)) continue;
+        float a[kSeg], b[kSeg];
+        values(st, a, b);
+        store_rows(reinterpret_cast<uint16_t*>(is_k ? kv.k : kv.v) + (block + c.row0 + r0 + st * kSeg) * kD, o1, o2, a, b);
       }
-      continue;
-    }
+    } else {
+      float* scale = (is_k ? kv.k_scale : kv.v_scale) + static_cast<long long>(c.page) * kv.n_heads + head;
+      const bool older = live && c.row0 > 0;
+      const float was = older ? *scale : 0.f;
+      float amax = 0.f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if (lane == 0) s_amax[par][warp] = amax;
-    float* scale = (is_k ? kv.k_scale : kv.v_scale) + static_cast<long long>(c.page) * kv.n_heads + head;
-    const bool older = live && c.row0 > 0;
-    const float was = older ? *scale : 0.f;
-    __syncthreads();  // also: every thread has read the old scale
-    if (!live) continue;
-    float m = 0.f;
-    for (int w = 0; w < team_warps; ++w) m = fmaxf(m, s_amax[par][team * team_warps + w]);
-    const int e = scale_exp(m);
-    float now = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-    float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    uint8_t* dst = (is_k ? kv.k : kv.v) + block * kD;
-    if (older) {
-      if (now > was) {
-        const float f = was * inv;
-        uint4* old = reinterpret_cast<uint4*>(dst);
-        for (int i = wt * 32 + lane; i < c.row0 * 4; i += team_warps * 32) {
-          uint4 v = old[i];
-          v.x = rescale4(v.x, f);
-          v.y = rescale4(v.y, f);
-          v.z = rescale4(v.z, f);
-          v.w = rescale4(v.w, f);
-          old[i] = v;
+      for (int st = 0; st < kSteps; ++st) {
+        if (!in(st)) continue;
+        float a[kSeg], b[kSeg];
+        values(st, a, b);
+        amax = largest(b, largest(a, amax));
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      if (lane == 0) s_amax[par][warp] = amax;
+      __syncthreads();  // also: every thread has read the old scale
+      if (live) {
+        float m = 0.f;
+        for (int x = 0; x < team_warps; ++x) m = fmaxf(m, s_amax[par][team * team_warps + x]);
+        const int e = scale_exp(m);
+        float to = power_of_two(e), inv = power_of_two(-e);
+        uint8_t* dst = (is_k ? kv.k : kv.v) + block * kD;
+        if (older) {
+          if (to > was) {
+            rescale_rows(dst, c.row0, was * inv, wt * 32 + lane, team_warps * 32);
+          } else {
+            to = was;
+            inv = 1.f / was;  // a power of two: exact
+          }
         }
-      } else {
-        now = was;
-        inv = 1.f / was;  // a power of two: exact
+        if (wt == 0 && lane == 0) *scale = to;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+          if (!in(st)) continue;
+          float a[kSeg], b[kSeg];
+          values(st, a, b);
+          uint8_t* row = dst + (c.row0 + r0 + st * kSeg) * kD;
+          store_codes(row + o1, a, inv);
+          store_codes(row + o2, b, inv);
+        }
       }
     }
-    if (wt == 0 && lane == 0) *scale = now;
+    now = next;
+  }
+}
+
+// Steps of single tokens: a few threads of a warp have a key or value row of one token and head, so that one wave of blocks
+// takes the whole step.
+template <bool kE4m3, int kSeg>
+__global__ void __launch_bounds__(32 * kWarps) append_token_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = 32 / kSeg;
+  const KvView& kv = p.kv;
+  const int lane = threadIdx.x & 31, g = lane % kLanes, rows = 2 * kv.n_heads;
+  const long long i = (static_cast<long long>(blockIdx.x) * (32 * kWarps) + threadIdx.x) / kLanes;
+  const int b = static_cast<int>(i / rows), task = static_cast<int>(i - static_cast<long long>(b) * rows);
+  const bool is_k = task < kv.n_heads;
+  const int head = is_k ? task : task - kv.n_heads;
+  const RopeTable& tb = p.rope;
+  int o1, o2;
+  segments<kSeg>(tb, is_k && p.has_rope, g, o1, o2);
+  SeqInfo s{0, 0, 0, false};
+  if (b < kv.n_seqs) s = seq_info(kv, b);
+  bool live = s.n_new > 0;
+  const int at = s.len - 1, r = at & (kv.page - 1);
+  int page = 0;
+  float x[kSeg], y[kSeg];
+  if (live) {
+    page = kv.table[static_cast<long long>(b) * kv.max_pages + (at >> kv.page_log2)];
+    Segment<uint16_t, kSeg> u, w;
+    const uint16_t* row = is_k ? p.k_rows + s.row0 * p.k_ts + head * p.k_hs : p.v_rows + s.row0 * p.v_ts + head * p.v_hs;
+    u.load(row + o1);
+    w.load(row + o2);
+    if (is_k && p.has_rope && g * kSeg < 4 * tb.n_groups) {
+      float sn[kSeg], cs[kSeg];
 #pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      if (!in[st]) continue;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = x[st][i];
-        x[st][i] = fabsf(a) <= kFltMax ? a * inv : __uint_as_float(0x7fffffffu);
-      }
-      uint8_t* row = dst + (wt * 16 + st * 4 + (lane >> 3)) * kD;
-      *reinterpret_cast<uint32_t*>(row + o1) = e4m3x4(x[st][0], x[st][1], x[st][2], x[st][3]);
-      *reinterpret_cast<uint32_t*>(row + o2) = e4m3x4(x[st][4], x[st][5], x[st][6], x[st][7]);
+      for (int j = 0; j < kSeg; ++j)
+        rope_sincos(tb, g * kSeg + j, p.pos[static_cast<long long>(s.row0) * tb.n_axes + tb.axis[(g * kSeg + j) >> 2]], sn[j], cs[j]);
+      spread(u, w, x, y);
+      turn(x, y, sn, cs, tb.interleaved);
+    } else {
+      spread(u, w, x, y);
     }
+    if (page < 0 || page >= kv.n_pages) {
+      atomicCAS(kv.err, 0, SAF3R_ERR_INDEX);
+      live = false;
+    }
+  }
+  const long long block = live ? (static_cast<long long>(page) * kv.n_heads + head) << kv.page_log2 : 0;  // first row
+  if constexpr (!kE4m3) {
+    if (live) store_rows(reinterpret_cast<uint16_t*>(is_k ? kv.k : kv.v) + (block + r) * kD, o1, o2, x, y);
+  } else {
+    float* scale = (is_k ? kv.k_scale : kv.v_scale) + (block >> kv.page_log2);
+    const bool older = live && r > 0;
+    const float was = older ? *scale : 0.f;
+    float m = live ? largest(y, largest(x, 0.f)) : 0.f;
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const int e = scale_exp(m);
+    float now = power_of_two(e), inv = power_of_two(-e);
+    const bool grows = older && now > was;
+    if (older && !grows) {
+      now = was;
+      inv = 1.f / was;  // a power of two: exact
+    }
+    uint8_t* dst = (is_k ? kv.k : kv.v) + block * kD;
+    // the whole warp rescales, row by row of those that need it
+    uint32_t todo = __ballot_sync(0xffffffffu, grows && g == 0);
+    while (todo) {
+      const int q = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const long long to = __shfl_sync(0xffffffffu, block, q);
+      const bool k = __shfl_sync(0xffffffffu, static_cast<int>(is_k), q) != 0;
+      rescale_rows((k ? kv.k : kv.v) + to * kD, __shfl_sync(0xffffffffu, r, q), __shfl_sync(0xffffffffu, was * inv, q), lane, 32);
+    }
+    if (!live) return;
+    if (g == 0) *scale = now;
+    store_codes(dst + r * kD + o1, x, inv);
+    store_codes(dst + r * kD + o2, y, inv);
+  }
+}
+
+template <int kSeg>
+void launch_append_seg(const AppendParams& p, bool e4m3, dim3 grid, size_t smem, cudaStream_t stream) {
+  if (p.kv.max_new == 1) {
+    if (e4m3)
+      append_token_kernel<true, kSeg><<<grid, 32 * kWarps, 0, stream>>>(p);
+    else
+      append_token_kernel<false, kSeg><<<grid, 32 * kWarps, 0, stream>>>(p);
+  } else if (e4m3) {
+    append_kernel<true, kSeg><<<grid, 32 * kWarps, smem, stream>>>(p);
+  } else {
+    append_kernel<false, kSeg><<<grid, 32 * kWarps, smem, stream>>>(p);
   }
 }
 
@@ -271,26 +395,31 @@ cudaError_t launch_append(const AppendParams& p0, bool e4m3, int num_sms, cudaSt
   AppendParams p = p0;
   const KvView& kv = p.kv;
   if (kv.n_seqs == 0 || kv.n_tokens == 0 || kv.max_new == 0) return cudaSuccess;
-  // the pages that can take new rows: new rows of a sequence touch at most (new - 2) / page + 2 pages
-  long long chunks = kv.n_seqs;
-  if (kv.max_new > 1) {
-    chunks = static_cast<long long>(kv.n_tokens) / kv.page + 2LL * kv.n_seqs;
+  const bool wide = !p.has_rope || p.rope.wide;
+  dim3 grid;
+  size_t smem = 0;
+  if (kv.max_new == 1) {
+    const long long threads = static_cast<long long>(kv.n_seqs) * 2 * kv.n_heads * (wide ? 4 : 8);
+    grid = dim3(static_cast<unsigned>((threads + 32 * kWarps - 1) / (32 * kWarps)));
+  } else {
+    // the pages that can take new rows: new rows of a sequence touch at most (new - 2) / page + 2 pages
+    long long chunks = static_cast<long long>(kv.n_tokens) / kv.page + 2LL * kv.n_seqs;
     const long long each = (kv.max_new - 2) / kv.page + 2;
     chunks = chunks < each * kv.n_seqs ? chunks : each * kv.n_seqs;
     chunks = chunks < kv.n_tokens ? chunks : kv.n_tokens;
+    // heads of a block share its sines: as many as leave 4 blocks for each SM, and at least what the teams take at once
+    const int teams = kWarps / (kv.page >> 4);
+    const int least = teams >= 2 ? teams / 2 : 1;
+    int hpb = kv.n_heads;
+    while (hpb > least && chunks * ((kv.n_heads + hpb - 1) / hpb) < 4LL * num_sms) hpb = (hpb + 1) / 2;
+    p.heads_per_block = hpb;
+    grid = dim3(static_cast<unsigned>(chunks), (kv.n_heads + hpb - 1) / hpb);
+    smem = p.has_rope ? static_cast<size_t>(kv.page) * 32 * sizeof(float2) : 0;
   }
-  // heads of a block share its sines: as many as leave a few blocks per SM, and at least what the teams take at once
-  const int teams = kWarps / (kv.page >> 4);
-  const int least = teams >= 2 ? teams / 2 : 1;
-  int hpb = kv.n_heads;
-  while (hpb > least && chunks * ((kv.n_heads + hpb - 1) / hpb) < 4LL * num_sms) hpb = (hpb + 1) / 2;
-  p.heads_per_block = hpb;
-  const dim3 grid(static_cast<unsigned>(chunks), (kv.n_heads + hpb - 1) / hpb);
-  const size_t smem = p.has_rope ? static_cast<size_t>(kv.page) * 32 * sizeof(float2) : 0;
-  if (e4m3)
-    append_kernel<true><<<grid, 32 * kWarps, smem, stream>>>(p);
+  if (wide)
+    launch_append_seg<8>(p, e4m3, grid, smem, stream);
   else
-    append_kernel<false><<<grid, 32 * kWarps, smem, stream>>>(p);
+    launch_append_seg<4>(p, e4m3, grid, smem, stream);
   ++*n_launch;
   return cudaGetLastError();
 }

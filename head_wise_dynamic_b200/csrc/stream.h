@@ -20,6 +20,8 @@ struct RopeTable {
   int32_t n_groups;
   int32_t interleaved;  // pairs (0,1),(2,3) of each half of a group, and o2 = o1 + 4; else (o1 + i, o2 + i)
   int32_t n_axes;
+  int32_t wide;         // groups 2q and 2q + 1 join to dims wide1[q]..+7 and wide2[q]..+7
+  int8_t wide1[4], wide2[4];
 };
 
 struct RopeParams {
