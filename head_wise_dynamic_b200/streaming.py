@@ -21,6 +21,15 @@ ROPE_HALF, ROPE_PAIRS, ROPE_SECTIONS = range(3)
 # saf3r_kv_type
 KV_BF16, KV_E4M3 = range(2)
 
+torch = None  # loaded by the first call or handle that takes tensors
+
+
+def _load_torch():
+    global torch
+    import torch as t
+    torch = t
+
+
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _ref = ctypes.byref
 
@@ -125,14 +134,14 @@ def _workspace(t, n: int, device):
 
 def _launch(device, stream, call, *args):
     """call(*args, stream) with the tensors' device as the current one; without `stream` on torch's current stream."""
-    import torch
     if device.type != "cuda":
         raise ValueError(f"CUDA tensors are wanted, got some on {device}")
+    index = device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
+        stream = torch._C._cuda_getCurrentRawStream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = call(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -148,7 +157,8 @@ class PagedKV:
     fp32 scales [n_pages, kv heads]).  The tensors stay the caller's."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
+        if torch is None:
+            _load_torch()
         _need(k.dim() == 4 and k.shape[3] == 64, "k: a pool [n_pages, kv heads, page, 64] is wanted")
         _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn), f"k: bfloat16 or float8_e4m3fn is wanted, got {k.dtype}")
         self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
@@ -167,7 +177,8 @@ class PagedKV:
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, page: int = 64, kv_type: int = KV_E4M3, device="cuda") -> "PagedKV":
         """A cache over newly allocated tensors (nothing in them needs a start value)."""
-        import torch
+        if torch is None:
+            _load_torch()
         shape = (n_pages, n_heads, page, 64)
         dt = torch.float8_e4m3fn if kv_type == KV_E4M3 else torch.bfloat16
         k, v = (torch.empty(shape, dtype=dt, device=device) for _ in range(2))
@@ -182,7 +193,8 @@ class KVBatch:
     tensors and the most new tokens of one sequence.  The tensors' contents may change between calls."""
 
     def __init__(self, cu_tokens, kv_lens, page_table, n_tokens: int, max_new: int):
-        import torch
+        if torch is None:
+            _load_torch()
         n = kv_lens.shape[0]
         self.cu_tokens, self.kv_lens, self.page_table, self.device = cu_tokens, kv_lens, page_table, kv_lens.device
         self.n_seqs, self.n_tokens, self.max_new = int(n), int(n_tokens), int(max_new)
@@ -192,6 +204,7 @@ class KVBatch:
             _dense(cu_tokens, torch.int32, (n + 1,), self.device, "cu_tokens"),
             _dense(kv_lens, torch.int32, (n,), self.device, "kv_lens"),
             _dense(page_table, torch.int32, (n, page_table.shape[1]), self.device, "page_table"))
+        self.workspace_bytes = {}
         self.ref = _ref(self.c)
 
 
@@ -201,7 +214,8 @@ def saf3r_rope(rope, x, pos, out, n_rot_heads: Optional[int] = None, inverse: bo
     """Rotate the first n_rot_heads heads (default: all) of x [tokens, heads, 64] by pos [tokens, axes]
     (int32) into out [tokens, heads, 64]; the other heads are copied.  x and out are bf16 or fp32, their rows
     in any order (out may be a transposed head-major tensor).  inverse: the adjoint."""
-    import torch
+    if torch is None:
+        _load_torch()
     T, H, dev = x.shape[0], x.shape[1], x.device
     xf, of = x.dtype == torch.float32, out.dtype == torch.float32
     _need((xf or x.dtype == torch.bfloat16) and (of or out.dtype == torch.bfloat16), "x and out: bfloat16 or float32")
@@ -215,7 +229,6 @@ def saf3r_rope(rope, x, pos, out, n_rot_heads: Optional[int] = None, inverse: bo
 def saf3r_kv_append(cache: PagedKV, batch: KVBatch, k, v, rope=None, pos=None, stream=None):
     """Append the step's rows k, v [n_tokens, kv heads, 64] (bf16) to the cache; with `rope` the keys
     are rotated by pos [n_tokens, axes] (int32) on the way."""
-    import torch
     dev, T, H = cache.device, batch.n_tokens, cache.n_heads
     _need(batch.device == dev and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16,
           "k and v: bfloat16 tensors, the batch on the cache's device")
@@ -239,14 +252,17 @@ def saf3r_kv_attn_workspace_bytes(cache: PagedKV, batch: KVBatch, window: saf3r_
 def saf3r_kv_attn(cache: PagedKV, batch: KVBatch, window: saf3r_window, q, out, workspace, stream=None):
     """Attention of the step's queries q [n_tokens, heads, 64] (bf16) over the cache, which holds the step's
     keys and values already, into out [n_tokens, heads, 64] (bf16 or fp32); rows in any order."""
-    import torch
     dev, T, H = cache.device, batch.n_tokens, q.shape[1]
     fp32 = out.dtype == torch.float32
     _need(batch.device == dev and q.dtype == torch.bfloat16 and (fp32 or out.dtype == torch.bfloat16),
           "q: bfloat16, out: bfloat16 or float32, the batch on the cache's device")
     qt, qh = _row_strides(q, T, H, dev, "q")
     ot, oh = _row_strides(out, T, H, dev, "out")
-    ws = _workspace(workspace, saf3r_kv_attn_workspace_bytes(cache, batch, window, H), dev)
+    sizes = (cache.n_heads, H)  # with the batch's own, all that the workspace depends on
+    need = batch.workspace_bytes.get(sizes)
+    if need is None:
+        need = batch.workspace_bytes[sizes] = saf3r_kv_attn_workspace_bytes(cache, batch, window, H)
+    ws = _workspace(workspace, need, dev)
     a = saf3r_query_rows(H, fp32, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh)
     _launch(dev, stream, _hw.lib().saf3r_kv_attn, cache.ref, batch.ref, _ref(window), _ref(a), ws)
 
@@ -260,7 +276,8 @@ def saf3r_window_attn_workspace_bytes(layout, window: saf3r_window) -> int:
 def saf3r_window_attn(layout, window: saf3r_window, q, k, v, out, workspace, stream=None):
     """Attention with a sliding window of views and sinks over q, k, v [H, N, 64] (bf16) held at once,
     into out [H, N, 64] (bf16 or fp32)."""
-    import torch
+    if torch is None:
+        _load_torch()
     L = _hw.layout_of(layout)
     dev, shape = q.device, (L.H, L.S * (L.grid_h * L.grid_w + L.n_special), L.d)
     fp32 = out.dtype == torch.float32
