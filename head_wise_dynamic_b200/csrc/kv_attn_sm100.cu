@@ -12,8 +12,8 @@
 //          core reads, a TMA box for each page (or 64 rows of it).  Value rows that no row of the item sees are cleared:
 //          what lies behind a sequence's end need not be finite.  bf16: TMA writes the stage itself.  8-bit: the
 //          codes land beside it, and four more warps (4-7) turn them into fp16 times their page's scale over the
-//          largest of the piece: exact where the scales are within 2^22 of one another, and the piece's rows go key by
-//          key where they are not.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
+//          largest of the piece: exact where the scales are within 2^22 of one another; where the values' are not, the piece's
+//          rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
 //   2-3    issue the products, a warp for each tile.
 //   last 16 softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
 //          Sixteen warps, four for each scheduler in different steps, hide each other's waits.
@@ -46,10 +46,11 @@ constexpr int kItem = 256;             // rows of an item
 constexpr int kRowBytes = 128;
 constexpr int kBlockBytes = 128 * kRowBytes;  // 128 rows x 64 bf16
 constexpr float kScaleLog2 = 0.18033688011112042f;  // log2(e) / sqrt(64)
-constexpr float kGrow = 16777216.f;    // a block's weights may sum to 2^24 before its rows' references move
+constexpr float kGrow = 1.8446744073709552e19f;  // a row with weights beyond 2^64 goes key by key
 constexpr float kGrowF16 = 32768.f;    // fp16 weights: 2^15
-constexpr int kCodeTop = 7;            // codes of a piece's largest scale are multiplied by 2^7 (448 * 2^7 is in fp16's range),
-constexpr int kWild = 22;              // those of scales down to 2^-22 of it by 2^-15 at least: exact in fp16, subnormal codes too
+// Codes of a piece's largest scale are multiplied by 2^7 (448 * 2^7 is in fp16's range), those of scales down to 2^-22 of it
+// by 2^-15 at least: exact in fp16, subnormal codes too.
+constexpr int kCodeTop = 7, kWild = 22;
 constexpr int kMaxShares = 160;        // CTAs of a launch at most (one for each SM)
 constexpr int kPlanEntries = 1024;
 // Cost of a key block and of an item's start and end, in sixteenths of a two-tile block.
@@ -57,7 +58,7 @@ constexpr int kCost2 = 16, kCost1 = 13, kCostItem = 16;
 constexpr int kLeastShare = 2 * kCost2;  // shares smaller than this are not worth a CTA
 
 // Pairs (of the 32 of a row's 64 keys) whose exponentials run on the FMA pipe.
-constexpr uint32_t kPolyPairs = 0x80808080u;
+constexpr uint32_t kPolyPairs = 0x10101010u;
 // p(f) = 1 + f (c1 + f (c2 + f c3)), fitted to 2^f on [0, 1) for least maximum relative error (8.6e-5)
 constexpr float kExpC1 = 0.6951168179512024f, kExpC2 = 0.22764486074447632f, kExpC3 = 0.07706713676452637f;
 
@@ -128,11 +129,11 @@ __device__ __forceinline__ int blocks_before(long long d, int nblk, int unit) {
 // Where share i of the line starts: the first `extra` shares have one unit more than `each`.
 __host__ __device__ __forceinline__ long long share_start(long long each, int extra, int i) { return each * i + (i < extra ? i : extra); }
 
-// 8-bit: what the codes of a block's groups of 16 keys are multiplied by, as pairs of fp16.
+// 8-bit: the scales of a block's groups of 16 keys: of the keys, then of the values.
 struct alignas(16) BlockScale {
-  uint32_t k[8], v[8];
+  float of[16];
 };
-// 8-bit: exponents of the largest scales of a piece's keys and values, and whether some scale is too small beside them.
+// 8-bit: exponents of the largest scales of a piece's keys and values, and whether some value scale is too small beside them.
 struct PieceScale {
   int k, v, wild;
 };
@@ -208,10 +209,10 @@ struct AttnSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t raw[kMaxStages], raw_empty[kMaxStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2][2], o_done[2], p_full[2][2];
+  uint64_t s_full[2][3], o_done[2], p_full[2][3];
   uint64_t drain[2];
   uint64_t pair[2][4];                // the two warps of a tile's 32 rows meet here
-  float stats[2][2][2][128][2];       // [piece parity][tile][half][row] = (reference, sum)
+  float2 stats[2][2][2][128];         // [parity][tile][half][row]: what the halves tell one another
   BlockScale scale[kScales];
   PieceScale piece_scale[kPieces];
   uint64_t scale_full[kPieces];
@@ -504,26 +505,27 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// 8-bit, warp 1: the largest scales of every piece.  A scale of 2^-100 is that of rows of zeros (or of values below 2^-91):
-// it does not count as too small.
+// 8-bit, warp 1: the largest scales of every piece.  Keys of far smaller scales may lose bits: 2^-41 of the largest key at
+// most, which no logit shows.  Values may not, as a row may see them alone.  A scale of 2^-100 is that of rows of zeros (or of
+// values below 2^-91): it does not count as too small.
 __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, int lane) {
   const KvView& kv = p.kv;
   Feed feed;
   while (const Piece* next = feed.next(p, sm)) {
     const Piece& pc = *next;
-    int k_hi = -127, v_hi = -127, k_lo = 127, v_lo = 127;
+    int k_hi = -127, v_hi = -127, v_lo = 127;
     const int per_log2 = 7 - p.box_log2;  // boxes of a block
-    // four boxes of a lane at a time: their entries, then their scales
-    for (int i0 = (pc.blk0 << per_log2) + lane; i0 < (pc.blk1 << per_log2); i0 += 128) {
-      int id[4];
-      float ks[4], vs[4];
+    // eight boxes of a lane at a time: their entries, then their scales
+    for (int i0 = (pc.blk0 << per_log2) + lane; i0 < (pc.blk1 << per_log2); i0 += 256) {
+      int id[8];
+      float ks[8], vs[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         const int i = i0 + 32 * c;
         id[c] = box_entry(p, pc, i >> per_log2, i & ((1 << per_log2) - 1));
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         const int i = i0 + 32 * c, row = box_row(p, pc, i >> per_log2, i & ((1 << per_log2) - 1), id[c]);
         ks[c] = vs[c] = 0.f;
         if (row >= 0) {
@@ -532,27 +534,25 @@ __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, i
         }
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         const int k = exponent(ks[c]), v = exponent(vs[c]);
         k_hi = max(k_hi, k);
         v_hi = max(v_hi, v);
-        if (k > -100) k_lo = min(k_lo, k);
         if (v > -100) v_lo = min(v_lo, v);
       }
     }
     k_hi = __reduce_max_sync(0xffffffffu, k_hi);
     v_hi = __reduce_max_sync(0xffffffffu, v_hi);
-    k_lo = __reduce_min_sync(0xffffffffu, k_lo);
     v_lo = __reduce_min_sync(0xffffffffu, v_lo);
     if (lane == 0) {
-      sm.piece_scale[feed.i % kPieces] = PieceScale{k_hi, v_hi, k_lo < k_hi - kWild || v_lo < v_hi - kWild};
+      sm.piece_scale[feed.i % kPieces] = PieceScale{k_hi, v_hi, v_lo < v_hi - kWild};
       mbar_arrive(&sm.scale_full[feed.i % kPieces]);
     }
     feed.done(sm, lane);
   }
 }
 
-// 8-bit, warp 0: every block's TMA boxes of codes into the ring of raw blocks, and what they are multiplied by.
+// 8-bit, warp 0: every block's TMA boxes of codes into the ring of raw blocks, and its scales.
 __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mk, const CUtensorMap* mv, int lane) {
   constexpr int kStages = Ring<true>::kStages, kRaw = Ring<true>::kRaw;
   const KvView& kv = p.kv;
@@ -573,8 +573,6 @@ __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem&
       sk = kv.k_scale[row >> kv.page_log2];
       sv = kv.v_scale[row >> kv.page_log2];
     }
-    if (!wait_all(p, sm, &sm.scale_full[pieces % kPieces], (pieces / kPieces) & 1)) break;
-    const PieceScale top = sm.piece_scale[pieces % kPieces];
     for (int blk = pc.blk0; blk < pc.blk1; ++blk, ++n) {
       const int next = box_row(p, pc, blk + 1, lane, entry);
       entry = box_entry(p, pc, blk + 2, lane);
@@ -591,8 +589,8 @@ __device__ __forceinline__ void load_codes_role(const KvAttnParams& p, AttnSmem&
       const int g = lane & 7, box = (16 * g) >> p.box_log2;
       const float of = __shfl_sync(0xffffffffu, sk, box), ov = __shfl_sync(0xffffffffu, sv, box);
       if (lane < 8) {
-        sm.scale[n % kScales].k[lane] = f16_power(exponent(of) - top.k);
-        sm.scale[n % kScales].v[lane] = f16_power(exponent(ov) - top.v);
+        sm.scale[n % kScales].of[lane] = of;
+        sm.scale[n % kScales].of[8 + lane] = ov;
       }
       __syncwarp();
       issue_boxes(p, mk, mv, pc, row, sm.ring + kStages * 2 * kBlockBytes + slot * kBlockBytes, &sm.raw[slot], kD, lane);
@@ -615,11 +613,15 @@ __device__ __forceinline__ void convert_role(const KvAttnParams& p, AttnSmem& sm
   uint32_t n = 0;
   while (const Piece* next = feed.next(p, sm)) {
     const int blk0 = next->blk0, blk1 = next->blk1;
+    if (!wait_all(p, sm, &sm.scale_full[feed.i % kPieces], (feed.i / kPieces) & 1)) return;
+    const int top = (lane & 8) ? sm.piece_scale[feed.i % kPieces].v : sm.piece_scale[feed.i % kPieces].k;
     for (int blk = blk0; blk < blk1; ++blk, ++n) {
       const uint32_t st = n % kStages, slot = n % kRaw;
       const bool whole = whole_block(*next, blk);
       if (!wait_all(p, sm, &sm.raw[slot], (n / kRaw) & 1)) return;
       if (n >= kStages && !wait_all(p, sm, &sm.empty[st], ((n / kStages) & 1) ^ 1)) return;
+      // lane g: what the keys of group g are multiplied by, lane 8 + g: the values
+      const uint32_t factors = f16_power(exponent(sm.scale[n % kScales].of[lane & 15]) - top);
       const uint8_t* src = sm.ring + kStages * 2 * kBlockBytes + slot * kBlockBytes + lane * 16;
       uint8_t* dst = sm.ring + st * 2 * kBlockBytes;
 #pragma unroll 1
@@ -637,7 +639,7 @@ __device__ __forceinline__ void convert_role(const KvAttnParams& p, AttnSmem& sm
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int u = u0 + i * kConverters;
-          const uint32_t f = sm.scale[n % kScales].k[u >> 1];  // two units a group; v follows k
+          const uint32_t f = __shfl_sync(0xffffffffu, factors, u >> 1);  // two units a group
           const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
           uint32_t h[8];
 #pragma unroll
@@ -747,6 +749,70 @@ __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, ui
   }
 }
 
+// The same with one accumulator for both key halves of a tile and three S buffers: a step is one key half of
+// one block, step n of the tile has buffer n % 3, and a buffer whose P V is issued takes the S of the third step after.
+template <bool kF16>
+__device__ __forceinline__ void mma_role_joint(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem_base, int t, int lane) {
+  constexpr uint32_t kStages = Ring<kF16>::kStages;
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, tmem_base) + t * 256, o_col = tmem + 192;
+  const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[t]), 16, 1024);
+  const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(smem_u32(sm.ring) + kBlockBytes, 8192, 1024);
+  Feed feed;
+  uint32_t n = 0, pieces = 0;  // key blocks of all pieces, pieces of this tile
+  uint32_t buf = 0, par = 0;     // of the next P
+  while (const Piece* pc = feed.next(p, sm)) {
+    const int nblk = __reduce_max_sync(0xffffffffu, pc->blk1 - pc->blk0);
+    const int rows = __reduce_max_sync(0xffffffffu, pc->rows);
+    feed.done(sm, lane);
+    if (rows <= t * 128) {  // the item has one tile: this warp lets everything go
+      for (int j = 0; j < nblk; ++j, ++n) {
+        if (!wait_all(p, sm, &sm.full[n % kStages], (n / kStages) & 1)) return;
+        if (lane == 0) mbar_arrive(&sm.empty[n % kStages]);
+      }
+      continue;
+    }
+    if (!wait_all(p, sm, &sm.q_full[t], pieces & 1)) return;
+    ++pieces;
+    const int steps = 2 * nblk;
+    // S of the piece's step i into buffer b
+    auto scores = [&](int i, uint32_t b) {
+      const uint32_t blk = n + (i >> 1);
+      if (!(i & 1) && !wait_all(p, sm, &sm.full[blk % kStages], (blk / kStages) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_qk<kF16>(q0, k0 + (blk % kStages) * kStageDesc + (i & 1) * (kTileDesc / 2), tmem + b * 64);
+        mma_commit(&sm.s_full[t][b]);
+        if (i == steps - 1) mma_commit(&sm.q_empty[t]);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int i = 0; i < 3 && i < steps; ++i)
+      if (!scores(i, buf + i >= 3 ? buf + i - 3 : buf + i)) return;
+    for (int i = 0; i < steps; ++i) {
+      if (!wait_all(p, sm, &sm.p_full[t][buf], par)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t cs = (n + (i >> 1)) % kStages;
+        const uint64_t dv = v0 + cs * kStageDesc + 512 * (i & 1);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(o_col, tmem + buf * 64 + kk * 8, dv + 128 * kk, idesc_of<kF16>(1), i > 0 || kk > 0 ? 1u : 0u);
+        if (i & 1) mma_commit(&sm.empty[cs]);
+        if (i == steps - 1) mma_commit(&sm.o_done[t]);
+      }
+      __syncwarp();
+      if (i + 3 < steps && !scores(i + 3, buf)) return;
+      if (++buf == 3) {
+        buf = 0;
+        par ^= 1;
+      }
+    }
+    n += nblk;
+  }
+}
+
 // ------------------------------------------------------------------ softmax
 
 __device__ __forceinline__ uint64_t range_bits(int a, int b) {
@@ -787,23 +853,26 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
   }
 }
 
-// Raises the rows' references to the largest logit of the chunk at least, and scales what was summed so far.  Returns
-// whether some row still has none (it has seen no key yet).
-__device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool first, uint64_t valid, float qs, float& m,
-                                              float& l) {
+// Largest logit that a row sees of a chunk.
+__device__ __forceinline__ float row_largest(uint32_t tS, uint64_t valid) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t s[16];
     tmem_ld16(tS + 16 * c, s);
     tmem_wait_ld();
-    float g = -INFINITY;
 #pragma unroll
     for (int q = 0; q < 16; ++q)
-      if ((valid >> (16 * c + q)) & 1ull) g = fmaxf(g, __uint_as_float(s[q]));
-    mx = fmaxf(mx, g * qs);
+      if ((valid >> (16 * c + q)) & 1ull) mx = fmaxf(mx, __uint_as_float(s[q]));
   }
-  const float now = fmaxf(m, mx);
+  return mx;
+}
+
+// Raises the rows' references to the largest logit of the chunk at least, and scales what was summed so far.  Returns
+// whether some row still has none (it has seen no key yet).
+__device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool first, uint64_t valid, float qs, float& m,
+                                              float& l) {
+  const float now = fmaxf(m, row_largest(tS, valid) * qs);
   const float alpha = now == m ? 1.f : fast_exp2(m - now);  // m may be -inf: alpha = 0
   m = now;
   l *= alpha;
@@ -833,15 +902,14 @@ __device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t vali
   }
 }
 
-// A row's 64 logits, 16 at a time, the next 16 on their way.
+// A row's 64 logits, 16 at a time, the next 16 on their way; the first 16 were asked for into `a`.
 template <bool kF16, bool kMask>
-__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, uint32_t (&pk)[32]) {
+__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, uint32_t (&a)[16], uint32_t (&pk)[32]) {
   const float add = m == -INFINITY ? 0.f : -m;
   constexpr uint32_t kPoly = kMask ? 0u : kPolyPairs;
   const uint32_t lo = static_cast<uint32_t>(valid), hi = static_cast<uint32_t>(valid >> 32);
   float rp[4] = {0.f, 0.f, 0.f, 0.f};
-  uint32_t a[16], b[16];
-  tmem_ld16(tS, a);
+  uint32_t b[16];
   tmem_wait_ld();
   tmem_ld16(tS + 16, b);
   weights16<kF16, (kPoly & 0xffu), kMask>(a, lo, qs, add, pk, rp);
@@ -908,6 +976,180 @@ __device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, 
   __syncwarp();
   if (lane == 0) mbar_arrive(&sm.q_full[t]);
   return true;
+}
+
+// Columns 32h..32h+31 of a piece's row: to the output, or to the share's slot.  (Run by a whole warp.)
+__device__ __forceinline__ void finish_row(const KvAttnParams& p, const Piece& pc, int row, int h, int tok, float mm, float den, bool part,
+                                           bool wild, const float (&o)[32], int lane) {
+  if (pc.slot >= 0) {
+    Slot& sl = reinterpret_cast<Work*>(p.ws)->slots[blockIdx.x][pc.slot];
+    float4* d = reinterpret_cast<float4*>(&sl.o[row][32 * h]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) d[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    if (h == 0) {
+      sl.m[row] = mm;
+      sl.l[row] = den;
+      sl.part[row] = (part ? 1 : 0) | (wild ? 2 : 0);
+    }
+    return;
+  }
+  const int a = pc.row0 + min(row, pc.rows - 1), head = pc.hk * p.group + a - tok * p.group;
+  const bool live = row < pc.rows;
+  bool bad = false;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) bad |= !(fabsf(o[q]) <= 3.402823466e+38f);
+  bad = (bad && part) || wild;
+  if (live && !bad) {
+    const long long at = (pc.s.row0 + tok) * p.out_ts + head * p.out_hs + 32 * h;
+    if (p.out_fp32) {
+      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) d[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    } else {
+      uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        d[q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                          pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+    }
+  }
+  // a value out of the row's sight is not finite (or one in sight is): key by key
+  uint32_t todo = __ballot_sync(0xffffffffu, live && bad);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int tk = __shfl_sync(0xffffffffu, tok, src), hd = __shfl_sync(0xffffffffu, head, src);
+    exact_row(p, pc.b, pc.s.len, pc.s.row0 + tk, pc.s.len - pc.s.n_new + tk, hd, lane, 32 * h, 32 * h + 32);
+  }
+}
+
+// The softmax of a tile whose key halves share a reference and an accumulator.  The halves' warps of 32 rows meet at a block
+// only while some of those rows have seen no key yet (a piece's first block, rows whose window begins later).  The
+// reference never moves after that: bf16 weights hold 2^64 over it, and a row beyond is done key by key.
+__device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem, int sw, int lane) {
+  const int t = sw >> 3, h = (sw >> 2) & 1, wq = sw & 3;
+  const int r = wq * 32 + lane;  // row of the tile
+  const uint32_t base = tmem + (static_cast<uint32_t>(wq * 32) << 16) + t * 256;
+  bool withhold = p.withhold != 0 && blockIdx.x == 0 && sw == 0;  // test hook
+  Feed feed;
+  uint32_t pieces = 0;
+  uint32_t buf = h, par = 0;  // this warp's next step
+  uint32_t meet = 0;
+  // the other half's value of this row
+  auto exchange = [&](float2 mine, float2& other) {
+    sm.stats[meet & 1][t][h][r] = mine;
+    mbar_arrive(&sm.pair[t][wq]);
+    if (!wait_all(p, sm, &sm.pair[t][wq], meet & 1)) return false;
+    other = sm.stats[meet & 1][t][h ^ 1][r];
+    ++meet;
+    return true;
+  };
+  const Piece* next = feed.next(p, sm);
+  if (next && !load_query<false>(p, sm, *next, 0, 0, t, h, r, lane)) return;
+  while (next) {
+    const Piece& pc = *next;
+    // the next piece's queries, before this one's end
+    auto look_ahead = [&]() {
+      Feed f = feed;
+      ++f.i;
+      next = f.next(p, sm);
+      return !next || load_query<false>(p, sm, *next, pieces, f.i % kPieces, t, h, r, lane);
+    };
+    if (pc.rows <= t * 128) {  // the item has one tile
+      if (!look_ahead()) return;
+      feed.done(sm, lane);
+      continue;
+    }
+    const int a = pc.row0 + min(t * 128 + r, pc.rows - 1), tok = p.by_group.div(a);
+    const Span sp = span_of(p.win, pc.s.len - pc.s.n_new + tok, pc.s.len);
+    float m = -INFINITY, l = 0.f;
+    bool unset = true;  // some row of the two warps has no reference yet
+    int flags = 0;      // 1: some streamed key is out of this row's sight, 2: weights beyond bf16's comfort
+    const Chunks ch = pc.ch;
+    const int blk0 = pc.blk0, blk1 = pc.blk1;
+    // what every row of the warp sees
+    const int all_lo = __reduce_max_sync(0xffffffffu, sp.lo), all_hi = __reduce_min_sync(0xffffffffu, sp.hi);
+    const int all_sink = __reduce_min_sync(0xffffffffu, sp.sink);
+    uint32_t first16[16];  // of the next S, on their way
+    auto start = [&]() {
+      if (!wait_all(p, sm, &sm.s_full[t][buf], par)) return false;
+      tc_fence_after();
+      tmem_ld16(base + buf * 64, first16);
+      return true;
+    };
+    if (!start()) return;
+    for (int blk = blk0;;) {
+      const int i = 2 * blk + h, j0 = ch.key(i);
+      const bool have = i < ch.total;
+      const bool all = have && ((j0 >= all_lo && j0 + 64 <= all_hi) || j0 + 64 <= all_sink);
+      uint64_t valid = ~0ull;
+      if (!all) {
+        valid = have ? range_bits(sp.lo - j0, sp.hi - j0) | range_bits(0, sp.sink - j0) : 0ull;
+        if (have && valid != ~0ull) flags |= 1;
+      }
+      const uint32_t tS = base + buf * 64;
+      const bool none = !all && __all_sync(0xffffffffu, valid == 0ull);
+      if (unset) {
+        tmem_wait_ld();
+        const float2 mine = make_float2(none ? -INFINITY : row_largest(tS, valid) * kScaleLog2, 0.f);
+        float2 other;
+        if (!exchange(mine, other)) return;
+        if (m == -INFINITY) m = fmaxf(mine.x, other.x);
+        unset = __any_sync(0xffffffffu, m == -INFINITY);
+      }
+      uint32_t pk[32];
+      if (none) {
+        // no row of this warp sees a key of the chunk
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 32; ++q) pk[q] = 0u;
+      } else {
+        const float sum = all ? weights<false, false>(tS, valid, m, kScaleLog2, first16, pk)
+                              : weights<false, true>(tS, valid, m, kScaleLog2, first16, pk);
+        if (sum > kGrow) flags |= 2;
+        l += sum;
+      }
+      tmem_st32(tS, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (withhold)
+        withhold = false;
+      else if (lane == 0)
+        mbar_arrive(&sm.p_full[t][buf]);
+      buf += 2;
+      if (buf >= 3) {
+        buf -= 3;
+        par ^= 1;
+      }
+      if (++blk == blk1) break;
+      if (!start()) return;
+      if (blk + 1 == blk1 && mbar_try_wait(&sm.piece_full[(feed.i + 1) % kPieces], ((feed.i + 1) / kPieces) & 1)) {
+        const Piece& nx = sm.pieces[(feed.i + 1) % kPieces];  // its queries, on their way to the caches
+        if (nx.blk1 >= 0 && t * 128 + r < nx.rows) prefetch_row(query_row(p, nx, t * 128 + r));
+      }
+    }
+    const uint32_t done = pieces & 1;
+    ++pieces;
+    if (!look_ahead()) return;
+    float2 other;
+    if (!exchange(make_float2(l, __int_as_float(flags)), other)) return;
+    if (!wait_all(p, sm, &sm.o_done[t], done)) return;
+    tc_fence_after();
+    flags |= __float_as_int(other.y);
+    const float den = l + other.x, scale = den == 0.f ? 0.f : 1.f / den;
+    float o[32];
+    {
+      uint32_t x[32];
+      tmem_ld32(base + 192 + 32 * h, x);
+      tmem_wait_ld();
+      tc_fence_before();
+#pragma unroll
+      for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(x[q]) * scale;
+    }
+    finish_row(p, pc, t * 128 + r, h, tok, m, den, (flags & 1) != 0, (flags & 2) != 0, o, lane);
+    feed.done(sm, lane);
+  }
 }
 
 template <bool kF16>
@@ -979,7 +1221,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
           if (raise) unset = new_reference(tS, tO + h * 64, first, valid, qs, m, l);
-          sum = all ? weights<kF16, false>(tS, valid, m, qs, pk) : weights<kF16, true>(tS, valid, m, qs, pk);
+          uint32_t first16[16];
+          tmem_ld16(tS, first16);
+          sum = all ? weights<kF16, false>(tS, valid, m, qs, first16, pk) : weights<kF16, true>(tS, valid, m, qs, first16, pk);
           raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)));  // far above the reference, or not a number
           if (!raise || pass == 1) break;
         }
@@ -998,16 +1242,14 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     ++pieces;
     if (!look_ahead()) return;
     // join the two key halves; this thread finishes columns 32h..32h+31 of its row
-    float* mine = sm.stats[par][t][h][r];
-    mine[0] = m;
-    mine[1] = part ? -l - 1e-30f : l;  // the sign says that some keys are out of sight
+    sm.stats[par][t][h][r] = make_float2(m, part ? -l - 1e-30f : l);  // the sign says that some keys are out of sight
     mbar_arrive(&sm.pair[t][wq]);
     if (!wait_all(p, sm, &sm.o_done[t], par)) return;
     if (!wait_all(p, sm, &sm.pair[t][wq], par)) return;
     tc_fence_after();
-    const float* other = sm.stats[par][t][h ^ 1][r];
-    const float mo = other[0], lo = fabsf(other[1]);
-    part |= other[1] < 0.f;
+    const float2 other = sm.stats[par][t][h ^ 1][r];
+    const float mo = other.x, lo = fabsf(other.y);
+    part |= other.y < 0.f;
     const bool wild = kF16 && sm.piece_scale[slot].wild != 0;
     const float mm = fmaxf(m, mo);
     const float fm = m == -INFINITY ? 0.f : fast_exp2(m - mm), fo = mo == -INFINITY ? 0.f : fast_exp2(mo - mm);
@@ -1025,48 +1267,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
 #pragma unroll
       for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(oa[q]) * f0 + __uint_as_float(ob[q]) * f1;
     }
-    const int row = t * 128 + r;
-    if (pc.slot >= 0) {
-      Slot& sl = reinterpret_cast<Work*>(p.ws)->slots[blockIdx.x][pc.slot];
-      float4* d = reinterpret_cast<float4*>(&sl.o[row][32 * h]);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) d[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-      if (h == 0) {
-        sl.m[row] = mm;
-        sl.l[row] = den;
-        sl.part[row] = (part ? 1 : 0) | (wild ? 2 : 0);
-      }
-      feed.done(sm, lane);
-      continue;
-    }
-    const int head = pc.hk * p.group + a - tok * p.group;
-    const bool live = row < pc.rows;
-    bool bad = false;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) bad |= !(fabsf(o[q]) <= 3.402823466e+38f);
-    bad = (bad && part) || wild;
-    if (live && !bad) {
-      const long long at = (pc.s.row0 + tok) * p.out_ts + head * p.out_hs + 32 * h;
-      if (p.out_fp32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) d[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-      } else {
-        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          d[q] = make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                            pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
-      }
-    }
-    // a value out of the row's sight is not finite (or one in sight is): key by key
-    uint32_t todo = __ballot_sync(0xffffffffu, live && bad);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int tk = __shfl_sync(0xffffffffu, tok, src), hd = __shfl_sync(0xffffffffu, head, src);
-      exact_row(p, pc.b, pc.s.len, pc.s.row0 + tk, pc.s.len - pc.s.n_new + tk, hd, lane, 32 * h, 32 * h + 32);
-    }
+    finish_row(p, pc, t * 128 + r, h, tok, mm, den, part, wild, o, lane);
     feed.done(sm, lane);
   }
 }
@@ -1095,7 +1296,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
       mbar_init(&sm.q_empty[t], 1);
       mbar_init(&sm.drain[t], 1);
       mbar_init(&sm.o_done[t], 1);
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 3; ++h) {
         mbar_init(&sm.s_full[t][h], 1);
         mbar_init(&sm.p_full[t][h], 4);
       }
@@ -1126,7 +1327,10 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
     if (kE4m3 && warp >= 4) {
       convert_role(p, sm, warp - 4, lane);
     } else if (warp >= 2) {
-      mma_role<kE4m3>(p, sm, tmem, warp - 2, lane);
+      if (kE4m3)
+        mma_role<kE4m3>(p, sm, tmem, warp - 2, lane);
+      else
+        mma_role_joint<kE4m3>(p, sm, tmem, warp - 2, lane);
       // also after a wait that gave up: no product is in flight when the block lets its memory go
       if (elect_one()) mma_commit(&sm.drain[warp - 2]);
       __syncwarp();
@@ -1145,7 +1349,10 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
       reg_alloc_inc<88>();
     else
       reg_alloc_inc<104>();
-    softmax_role<kE4m3>(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
+    if (kE4m3)
+      softmax_role<kE4m3>(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
+    else
+      softmax_role_joint(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
   }
   __syncwarp();
   tc_fence_before();

@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const ItemRec rec = recs(p)[item_index(p, blockIdx.y, hk, rg, R)];
   const int i0 = rec.first, i1 = rec.last;
-  if (i0 == i1) return;  // one warp had the whole item
+  if (i0 == i1 || i0 < 0 || i1 >= kMaxShares) return;  // one warp had the whole item (or, after a wait that gave up, none)
   const int turn = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;  // warps of a row
   const int at0 = warp & (turn - 1);
   const Slot* base = slots(p);
