@@ -53,25 +53,24 @@ __device__ __forceinline__ void spread(const Segment<T, N>& u, const Segment<T, 
   }
 }
 
-// Turns the segments' N pairs: (a[i], b[i]), or neighbours inside each segment.
-template <int N>
-__device__ __forceinline__ void turn(float (&a)[N], float (&b)[N], const float (&s)[N], const float (&c)[N], bool interleaved) {
+// Turns the segments' N pairs: (a[i], b[i]), or neighbours inside each segment.  T: what the products are held in.
+template <typename T>
+__device__ __forceinline__ void turn_pair(float& a, float& b, T s, T c) {
+  const T x = a, y = b;
+  a = static_cast<float>(x * c - y * s);
+  b = static_cast<float>(x * s + y * c);
+}
+template <typename T, int N>
+__device__ __forceinline__ void turn(float (&a)[N], float (&b)[N], const T (&s)[N], const T (&c)[N], bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const float a0 = a[2 * i], a1 = a[2 * i + 1], b0 = b[2 * i], b1 = b[2 * i + 1];
-      a[2 * i] = a0 * c[i] - a1 * s[i];
-      a[2 * i + 1] = a0 * s[i] + a1 * c[i];
-      b[2 * i] = b0 * c[N / 2 + i] - b1 * s[N / 2 + i];
-      b[2 * i + 1] = b0 * s[N / 2 + i] + b1 * c[N / 2 + i];
+      turn_pair(a[2 * i], a[2 * i + 1], s[i], c[i]);
+      turn_pair(b[2 * i], b[2 * i + 1], s[N / 2 + i], c[N / 2 + i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = x * c[i] - y * s[i];
-      b[i] = x * s[i] + y * c[i];
-    }
+    for (int i = 0; i < N; ++i) turn_pair(a[i], b[i], s[i], c[i]);
   }
 }
 

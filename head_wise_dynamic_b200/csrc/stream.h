@@ -165,11 +165,52 @@ __device__ __forceinline__ Chunks chunks_of(const Runs& r) {
   return c;
 }
 
-__device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int pos, float& s, float& c) {
+// The angle pos * freq as a signed part of a quarter turn from the nearest one: r * 2^-64, and which quarter.
+__device__ __forceinline__ int64_t rope_angle(const RopeTable& t, int pair, int pos, uint32_t& quarter) {
   const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * t.freq[pair];
-  // upper 32 bits as a signed fraction of a turn, in half turns: [-1, 1)
-  const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;
-  sincospif(x, &s, &c);
+  quarter = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
+  return static_cast<int64_t>(turn << 2);
+}
+template <typename T>
+__device__ __forceinline__ void to_quarter(uint32_t quarter, T& s, T& c) {
+  if (quarter & 1) {
+    const T x = s;
+    s = c;
+    c = -x;
+  }
+  if (quarter & 2) {
+    s = -s;
+    c = -c;
+  }
+}
+__device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int pos, float& s, float& c) {
+  uint32_t quarter;
+  const int64_t r = rope_angle(t, pair, pos, quarter);
+  // the upper 32 bits, in half turns: [-1/4, 1/4)
+  sincospif(static_cast<float>(static_cast<int32_t>(r >> 32)) * 1.1641532182693481e-10f, &s, &c);
+  to_quarter(quarter, s, c);
+}
+// The same in 64 bits, by the sine's and cosine's series: |x| <= pi / 4, so the terms left out are below 1e-15.
+__device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int pos, double& s, double& c) {
+  uint32_t quarter;
+  const double x = static_cast<double>(rope_angle(t, pair, pos, quarter)) * (1.5707963267948966 / 18446744073709551616.0);
+  const double y = x * x;
+  double a = -1.0 / 1307674368000.0, b = -1.0 / 87178291200.0;
+  a = fma(a, y, 1.0 / 6227020800.0);
+  b = fma(b, y, 1.0 / 479001600.0);
+  a = fma(a, y, -1.0 / 39916800.0);
+  b = fma(b, y, -1.0 / 3628800.0);
+  a = fma(a, y, 1.0 / 362880.0);
+  b = fma(b, y, 1.0 / 40320.0);
+  a = fma(a, y, -1.0 / 5040.0);
+  b = fma(b, y, -1.0 / 720.0);
+  a = fma(a, y, 1.0 / 120.0);
+  b = fma(b, y, 1.0 / 24.0);
+  a = fma(a, y, -1.0 / 6.0);
+  b = fma(b, y, -0.5);
+  s = fma(a * y, x, x);
+  c = fma(b, y, 1.0);
+  to_quarter(quarter, s, c);
 }
 
 #endif
