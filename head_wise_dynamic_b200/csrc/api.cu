@@ -727,6 +727,22 @@ bool saf3r::make_map_rows(CUtensorMap* m, const void* base, long long rows, long
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 query rows as [kv heads][tokens][heads of a group][64], any strides (elements), boxes of box_tokens tokens of a group,
+// 128-byte swizzle, zero fill.
+bool saf3r::make_map_queries(CUtensorMap* m, const void* q, int group, int n_tokens, int kv_heads, long long token_stride,
+                             long long head_stride, int box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || token_stride < 64 || head_stride < 64) return false;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(group), static_cast<cuuint64_t>(n_tokens), static_cast<cuuint64_t>(kv_heads)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(token_stride) * 2,
+                           static_cast<cuuint64_t>(head_stride) * group * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(box_tokens), 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [rows][64] 8-bit codes, box_rows x 64 boxes, as they are or with 64-byte swizzle.
 bool saf3r::make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows, bool swizzle) {
   EncodeTiledFn enc = encode_fn();

@@ -53,8 +53,8 @@ constexpr float kGrowF16 = 32768.f;    // fp16 weights: 2^15
 constexpr int kCodeTop = 7, kWild = 22;
 constexpr int kMaxShares = 160;        // CTAs of a launch at most (one for each SM)
 constexpr int kPlanEntries = 1024;
-// Cost of a key block and of an item's start and end, in sixteenths of a two-tile block.
-constexpr int kCost2 = 16, kCost1 = 13, kCostItem = 16;
+// Cost of a key block of two tiles and of one (which waits more), and of an item's start and end, in sixteenths of the first.
+constexpr int kCost2 = 16, kCost1 = 13, kCostItem = 56;
 constexpr int kLeastShare = 2 * kCost2;  // shares smaller than this are not worth a CTA
 
 // Pairs (of the 32 of a row's 64 keys) whose exponentials run on the FMA pipe.
@@ -454,17 +454,42 @@ __device__ __forceinline__ void load_role(const KvAttnParams& p, AttnSmem& sm, c
   }
 }
 
-// bf16, warp 1: zeros over the values of partial blocks that no row sees (what lies there need not be finite).
-__device__ __forceinline__ void clear_role(const KvAttnParams& p, AttnSmem& sm, int lane) {
+// bf16, warp 1: the pieces' queries where TMA takes them (p.q_tma), and zeros over the values of partial blocks that no row
+// sees (what lies there need not be finite).
+__device__ __forceinline__ void side_role(const KvAttnParams& p, AttnSmem& sm, const CUtensorMap* mq, int lane) {
   constexpr int kStages = Ring<false>::kStages;
   Feed feed;
-  uint32_t n = 0, raw = 0;
+  uint32_t n = 0, raw = 0, queries[2] = {0, 0};
+  auto drain = [&]() {  // every copy has landed before the block exits
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (queries[t] > 0) mbar_wait_drain(&sm.q_full[t], (queries[t] & 1) ^ 1, kDrainBudget);
+  };
   while (const Piece* next = feed.next(p, sm)) {
     const Piece& pc = *next;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (!p.q_tma || pc.rows <= t * 128) continue;
+      if (queries[t] > 0 && !wait_all(p, sm, &sm.q_empty[t], (queries[t] & 1) ^ 1)) {
+        drain();
+        return;
+      }
+      ++queries[t];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full[t], kBlockBytes);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)  // 64 rows: the heads of the group, token after token
+          tma_load_4d(sm.q[t] + i * kBlockBytes / 2, mq, 0, 0, pc.s.row0 + p.by_group.div(pc.row0 + t * 128 + i * 64), pc.hk, &sm.q_full[t]);
+      }
+      __syncwarp();
+    }
     for (int blk = pc.blk0; blk < pc.blk1; ++blk, ++n) {
       if (whole_block(pc, blk)) continue;
       const uint32_t st = n % kStages;
-      if (!wait_all(p, sm, &sm.raw[st], (raw >> st) & 1u)) return;
+      if (!wait_all(p, sm, &sm.raw[st], (raw >> st) & 1u)) {
+        drain();
+        return;
+      }
       raw ^= 1u << st;
       const uint32_t v = smem_u32(sm.ring + st * 2 * kBlockBytes + kBlockBytes);
 #pragma unroll 1
@@ -479,6 +504,7 @@ __device__ __forceinline__ void clear_role(const KvAttnParams& p, AttnSmem& sm, 
     }
     feed.done(sm, lane);
   }
+  drain();
 }
 
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
@@ -936,7 +962,7 @@ __device__ __forceinline__ void prefetch_row(const void* src) { asm volatile("pr
 template <bool kF16>
 __device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, const Piece& pc, uint32_t i, uint32_t slot, int t,
                                            int h, int r, int lane) {
-  if (pc.rows <= t * 128) return true;
+  if (pc.rows <= t * 128 || p.q_tma) return true;
   if (i >= 1 && !wait_all(p, sm, &sm.q_empty[t], (i & 1) ^ 1)) return false;
   const int row = t * 128 + r;
   {
@@ -1124,7 +1150,7 @@ __device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSm
       }
       if (++blk == blk1) break;
       if (!start()) return;
-      if (blk + 1 == blk1 && mbar_try_wait(&sm.piece_full[(feed.i + 1) % kPieces], ((feed.i + 1) / kPieces) & 1)) {
+      if (blk + 1 == blk1 && !p.q_tma && mbar_try_wait(&sm.piece_full[(feed.i + 1) % kPieces], ((feed.i + 1) / kPieces) & 1)) {
         const Piece& nx = sm.pieces[(feed.i + 1) % kPieces];  // its queries, on their way to the caches
         if (nx.blk1 >= 0 && t * 128 + r < nx.rows) prefetch_row(query_row(p, nx, t * 128 + r));
       }
@@ -1275,7 +1301,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
 template <bool kE4m3>
 __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
     kv_attn_kernel(const __grid_constant__ KvAttnParams p, const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v) {
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q) {
   extern __shared__ uint8_t smem_raw[];
   AttnSmem& sm = *reinterpret_cast<AttnSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1292,7 +1318,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
         mbar_init(&sm.piece_empty[2 * i + t], Ring<kE4m3>::kWarps - 1);
         mbar_init(&sm.scale_full[2 * i + t], 1);
       }
-      mbar_init(&sm.q_full[t], 8);
+      mbar_init(&sm.q_full[t], p.q_tma ? 1 : 8);
       mbar_init(&sm.q_empty[t], 1);
       mbar_init(&sm.drain[t], 1);
       mbar_init(&sm.o_done[t], 1);
@@ -1342,7 +1368,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
     } else if (kE4m3) {
       scan_role(p, sm, lane);
     } else {
-      clear_role(p, sm, lane);
+      side_role(p, sm, &map_q, lane);
     }
   } else {
     if (kE4m3)
@@ -1444,13 +1470,17 @@ saf3r_status launch_attn(const KvAttnParams& p0, cudaStream_t stream, int* n_lau
     ok = p.e4m3 ? make_map_codes(&mk, kv.k, rows, box, false) && make_map_codes(&mv, kv.v, rows, box, false)
                 : make_map_rows(&mk, kv.k, rows, kD, 1, rows * kD, box) && make_map_rows(&mv, kv.v, rows, kD, 1, rows * kD, box);
   }
+  // queries by TMA: 64 rows are whole tokens of a group (bf16 products only: 8-bit caches want them as fp16)
+  CUtensorMap mq = mk;
+  p.q_tma = !p.e4m3 && p.group <= 64 && (p.group & (p.group - 1)) == 0 &&
+            make_map_queries(&mq, p.q, p.group, kv.n_tokens, kv.n_heads, p.q_ts, p.q_hs, 64 / p.group);
   if (!ok) return SAF3R_ERR_CUDA;
   const int smem = static_cast<int>(sizeof(AttnSmem) + 1024);
   const auto kernel = p.e4m3 ? kv_attn_kernel<true> : kv_attn_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return SAF3R_ERR_CUDA;
   const int grid = p.num_sms < kMaxShares ? p.num_sms : kMaxShares;
-  kernel<<<grid, 32 * (p.e4m3 ? Ring<true>::kWarps : Ring<false>::kWarps), smem, stream>>>(p, mk, mv);
+  kernel<<<grid, 32 * (p.e4m3 ? Ring<true>::kWarps : Ring<false>::kWarps), smem, stream>>>(p, mk, mv, mq);
   ++*n_launch;
   if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
   if (grid > 1) {

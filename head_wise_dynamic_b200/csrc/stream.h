@@ -101,6 +101,7 @@ struct KvAttnParams {
   int32_t withhold;
   int32_t least_share; // few rows: chunks that are worth a warp
   int32_t box_log2;    // keys of one TMA box
+  int32_t q_tma;       // tensor cores: the queries come by TMA
 };
 
 #ifdef __CUDACC__
@@ -236,6 +237,8 @@ long long call_wait_budget();
 bool take_withhold_arrive();
 bool make_map_rows(CUtensorMap* m, const void* base, long long rows, long long row_stride, int heads,
                    long long head_stride, int box_rows);
+bool make_map_queries(CUtensorMap* m, const void* q, int group, int n_tokens, int kv_heads, long long token_stride,
+                      long long head_stride, int box_tokens);
 bool make_map_codes(CUtensorMap* m, const void* base, long long rows, int box_rows, bool swizzle);
 
 }  // namespace saf3r
