@@ -150,7 +150,7 @@ __device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long lon
   const int per = (n + kThreads - 1) / kThreads;
   long long mine = 0;
   for (int b = threadIdx.x * per; b < min(static_cast<int>(threadIdx.x + 1) * per, n); ++b)
-    mine += seq_head_cost(p, seq_info(p.kv, b), R) * p.kv.n_heads;
+    mine += seq_head_cost(p, seq_info(p.kv, b), R);  // of one kv head
   long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -162,6 +162,7 @@ __device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long lon
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += entries[32 * w + 31];
+  total *= p.kv.n_heads;
   const int most = gridDim.x * kWarps;
   const int shares = total >= static_cast<long long>(most) * p.least_share ? most : max(1, static_cast<int>(total) / p.least_share);
   // (a 64-bit division takes several times as long)
@@ -177,23 +178,24 @@ __device__ __forceinline__ Walk make_walk(const KvAttnParams& p, int R, long lon
   w.xe = me < shares ? share_start(me + 1) : total;
   w.x = w.xs;
   if (w.xs >= w.xe) return w;
-  long long rest = w.xs;
+  long long rest = w.xs, head = 0;  // head: cost of the sequence for one kv head
   for (int q = 0; q < kWarps; ++q) {
     const long long in = entries[32 * q + lane];
-    const uint32_t hit = __ballot_sync(0xffffffffu, rest < in);
+    const uint32_t hit = __ballot_sync(0xffffffffu, rest < in * p.kv.n_heads);
     if (hit) {
       const int src = __ffs(hit) - 1;
+      const long long before = src > 0 ? entries[32 * q + src - 1] : 0;
       w.b = (32 * q + src) * per;
-      if (src > 0) rest -= entries[32 * q + src - 1];
+      head = entries[32 * q + src] - before;
+      rest -= before * p.kv.n_heads;
       break;
     }
-    rest -= entries[32 * q + 31];
+    rest -= entries[32 * q + 31] * p.kv.n_heads;
   }
-  long long head = 0;
-  for (;; ++w.b) {
-    w.s = seq_info(p.kv, w.b);
+  w.s = seq_info(p.kv, w.b);
+  for (; per > 1; w.s = seq_info(p.kv, ++w.b)) {
     head = seq_head_cost(p, w.s, R);
-    if (per == 1 || w.b + 1 >= n || rest < head * p.kv.n_heads) break;
+    if (w.b + 1 >= n || rest < head * p.kv.n_heads) break;
     rest -= head * p.kv.n_heads;
   }
   while (rest >= head && w.hk + 1 < p.kv.n_heads) {
