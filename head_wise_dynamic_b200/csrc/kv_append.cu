@@ -2,14 +2,18 @@
 //
 // A block owns one page of one sequence that takes new rows, for some of the kv heads: 8 warps in
 // teams of page / 16, each team one head's keys or values, a warp 16 rows of the page.  A team
-// holds its rows in registers in fp32 between the largest magnitude (8-bit caches: it fixes the
-// page's scale) and the store, so every row is read once.  Sines and cosines are computed once per block
-// and row and shared by its heads.  Because one block owns a (page, head), growing a scale and
-// re-rounding the older rows needs no atomics.  Bound by memory for whole views, by launch and
-// latency for single tokens.
+// holds its rows in registers between the largest magnitude (8-bit caches: it fixes the
+// page's scale) and the store, so every row is read once, and has the next task's rows on their way meanwhile.  Sines and
+// cosines are computed once per block and row and shared by its heads.  Because one block owns a (page, head), growing a scale
+// and re-rounding the older rows needs no atomics.
 //
 // Scales are powers of two: x / scale is exact, and re-rounding older codes when a scale grows is too
 // unless they become subnormal.
+//
+// Measured: 16 views of bf16 (1,374 tokens, 16 heads, pages of 16) 39 us, 70% of the measured copy rate: 4 loads that wait
+// for one another before a block's first row is stored, three waves of blocks.  Fewer heads a block cost more
+// (8: 44 us, 4: 60 us), as does putting the rows together in shared memory first (45 us).  One 8-bit view 14 us and 64 single tokens
+// 4.3 us of GPU time (a call takes 7.6 us of the host): latency.
 #include "rope.cuh"
 #include "stream.h"
 

@@ -12,18 +12,24 @@
 //          core reads, a TMA box for each page (or 64 rows of it).  Value rows that no row of the item sees are cleared:
 //          what lies behind a sequence's end need not be finite.  bf16: TMA writes the stage itself.  8-bit: the
 //          codes land beside it, and four more warps (4-7) turn them into fp16 times their page's scale over the
-//          largest of the piece: exact where the scales are within 2^22 of one another; where the values' are not, the piece's
-//          rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
+//          largest of the piece: exact where the scales are within 2^22 of one another; where the values' are not, the
+//          piece's rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
 //   2-3    issue the products, a warp for each tile.
 //   last 16 softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
 //          Sixteen warps, four for each scheduler in different steps, hide each other's waits.
-// Tensor memory (512 columns): for each tile S (128 fp32 columns; each half's P, bf16 or fp16, goes over the first 32
-// columns of its half once read) and an accumulator O for each key half (64 columns).  The halves have a
-// reference and sum of their own and meet when the piece ends.
+// Tensor memory (512 columns, 256 a tile).  bf16: three S buffers of 64 fp32 columns (P, bf16, goes over the first 32 columns
+// of its S once read) and one accumulator O of 64 columns, whose halves share a reference.  8-bit: S and O for each key half.
 //
 // Weights are 2^(x - reference), the reference a row's largest logit of its first block: bf16 P and the fp32 sums
-// keep their relative precision at any reference, so no maximum is taken of later blocks.  Only a block whose
-// weights sum to more than 2^24 (fp16: 2^15) moves it: its logits are read again, what was summed so far is scaled.
+// keep their relative precision at any reference, so no maximum is taken of later blocks.  bf16 weights may grow to 2^64
+// (a row beyond goes key by key); fp16 ones to 2^15, then the reference moves and what was summed so far is scaled.
+//
+// What bounds it: at d = 64 each (query, key) pair is 256 tensor operations and one exponential, and the softmax warps' pipes
+// set the pace: per block of 256 rows and 128 keys 1,792 cycles of the exponential unit (one pair in eight is computed on the
+// FMA pipe: none took 604 us, one in four 571 us, one in eight 556 us) of about 2,350; products take 1,264.  Measured, 16 heads,
+// bf16: 549 us for 10,992 rows and keys = 902 TFLOP/s, 55% of the measured burst rate; long runs meet the power cap and
+// end near 1.5 GHz and 700 TFLOP/s.  8-bit: 237 us for 2 x 1,374 rows over 12,366 keys = 587 TFLOP/s, where the converting
+// warps take the schedulers' slots as well.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

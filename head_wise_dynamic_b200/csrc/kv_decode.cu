@@ -18,6 +18,11 @@
 // is the weight times vs, and the row's sum takes P / vs.  bf16 caches use bf16 products throughout.
 // The reference is the largest x of the first step; it moves when a later one exceeds it by 2^15
 // (fp16 P, which ends 2^-24 below it) or 2^24.
+//
+// Measured, 64 8-bit streams of 1 to 22,000 keys, 4 kv heads of 4 query heads: 77 us with the join, 71% of the measured copy
+// rate.  In its stride a warp's step of 8 KB takes 3,660 cycles with 12 warps an SM, more than that rate;
+// the first step ends 12,000 cycles after the start (lengths, page, scales and codes are four loads that wait for one another).  16-row
+// products straight from global memory, without the transposition, took 216 us.
 #include <cuda.h>
 
 #include "ptx.cuh"

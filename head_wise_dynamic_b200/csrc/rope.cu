@@ -92,8 +92,8 @@ constexpr int kThreads = 256;
 
 // A thread owns two segments of kSeg values of one token's rows (kSeg pairs): 8 where the pairing's halves are
 // aligned to 8 values, else 4.  It asks for its first heads' rows before it works out the angles, and has
-// 128 bytes of rows on their way at a time.  Measured (43,968 tokens, 48 heads, bf16): 000 us, with
-// 4-value segments and 64 bytes on their way 135 us.
+// 128 bytes of rows on their way at a time.  Measured (43,968 tokens, 48 heads, bf16): 89 us, 93% of a plain
+// copy's rate; with 4-value segments and 64 bytes on their way 136 us.
 template <typename In, typename Out, int kSeg>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kLanes = 32 / kSeg;  // threads of a row

@@ -428,8 +428,11 @@ size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv
 /*
  * Attention of each sequence's new tokens to its cached tokens, themselves among them (append first):
  * softmax(q . k / sqrt(64)) over the tokens that `window` lets them see.  Pages without a visible token are not
- * read: the caller may have given them to others.  Few rows per sequence (max_new * heads per kv head up to a limit)
- * take a kernel that splits the keys over the GPU; others the tensor-core kernel.
+ * read: the caller may have given them to others.  Up to 64 rows per sequence and kv head (max_new * heads per kv head)
+ * take a kernel that splits the keys over the GPU; more the tensor-core kernel.  Weights are rounded once, to bf16 or, over 8-bit
+ * caches, to fp16 (where those below 2^-14 of a row's first logits' largest weight lose bits, 2^-25 of it at most); sums
+ * are in fp32.  What a masked token holds never reaches a row: next to one whose values are not finite, and where the
+ * value scales of a row's pages are more than 2^22 apart, rows are computed key by key, at a small fraction of the speed.
  * workspace: DEVICE, 16-byte aligned, saf3r_kv_attn_workspace_bytes bytes, used by one call at a time
  * (also when calls are captured: graphs that share it must not overlap); it needs no start value.
  */
@@ -457,7 +460,7 @@ void saf3r_set_kernel_events(void* start, void* stop);
 
 /*
  * Budget, in GPU clock cycles, of every bounded device wait (the attention
- * kernel's and the token-wise selection's pipeline waits) in the calls that
+ * kernels' and the token-wise selection's pipeline waits) in the calls that
  * follow on this host thread; cycles <= 0 restores the default of 4e9 cycles
  * (about 2 s at 1.965 GHz).  When a wait runs out, its CTA records
  * SAF3R_ERR_TIMEOUT in the device error word, lets the copies it has in flight
@@ -467,8 +470,9 @@ void saf3r_set_kernel_events(void* start, void* stop);
 void saf3r_set_wait_budget(long long cycles);
 
 /*
- * Test hook for the timeout path.  The next saf3r_sparse_attn or
- * saf3r_dense_attn call on this host thread launches its attention kernel with
+ * Test hook for the timeout path.  The next saf3r_sparse_attn, saf3r_dense_attn,
+ * saf3r_window_attn or (with its tensor-core kernel) saf3r_kv_attn call on this
+ * host thread launches its attention kernel with
  * one softmax warp of the first CTA withholding its first "P is in tensor
  * memory" arrival, so the tensor-core warp's wait for it runs out after the wait
  * budget (see saf3r_set_wait_budget): nothing faults or hangs, every device wait
