@@ -27,6 +27,11 @@ bool strides_ok(long long tokens, long long ts, long long heads, long long hs, b
   return true;
 }
 
+bool apart(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + na <= y || y + nb <= x;
+}
+
 saf3r_status check_cache(const saf3r_kv_cache* c, bool pointers) {
   if (!c) return SAF3R_ERR_INVALID;
   if (c->n_pages < 1 || c->n_heads < 1 || c->n_heads > kMaxHeads) return SAF3R_ERR_INVALID;
@@ -190,6 +195,8 @@ saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* ba
   if (batch->n_seqs == 0 || batch->n_tokens == 0 || batch->max_new == 0) return SAF3R_OK;
   if (!rows->q || !rows->out || !workspace || !aligned16(rows->q) || !aligned16(rows->out) || !aligned16(workspace))
     return SAF3R_ERR_INVALID;
+  // a row may be computed again after others of its tile were written, from the queries
+  if (rows->out == rows->q) return SAF3R_ERR_INVALID;
   if (!strides_ok(batch->n_tokens, rows->q_token_stride, rows->n_heads, rows->q_head_stride, false, true) ||
       !strides_ok(batch->n_tokens, rows->out_token_stride, rows->n_heads, rows->out_head_stride, rows->out_is_fp32 != 0,
                   true))
@@ -238,9 +245,12 @@ saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* w
   if (!window_ok(window) || !q || !k || !v || !out || !workspace || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
       !aligned16(out) || !aligned16(workspace))
     return SAF3R_ERR_INVALID;
+  const Dims d = make_dims(*layout);
+  const size_t n = static_cast<size_t>(d.H) * d.N * kD, out_bytes = n * (out_is_fp32 ? 4 : 2);
+  if (!apart(out, out_bytes, q, 2 * n) || !apart(out, out_bytes, k, 2 * n) || !apart(out, out_bytes, v, 2 * n))
+    return SAF3R_ERR_INVALID;
   int sms = 0, *err = nullptr;
   if ((st = device(&sms, &err)) != SAF3R_OK) return st;
-  const Dims d = make_dims(*layout);
   KvAttnParams p;
   std::memset(&p, 0, sizeof(p));
   p.kv.err = err;

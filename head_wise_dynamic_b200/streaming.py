@@ -251,7 +251,7 @@ def saf3r_kv_attn_workspace_bytes(cache: PagedKV, batch: KVBatch, window: saf3r_
 
 def saf3r_kv_attn(cache: PagedKV, batch: KVBatch, window: saf3r_window, q, out, workspace, stream=None):
     """Attention of the step's queries q [n_tokens, heads, 64] (bf16) over the cache, which holds the step's
-    keys and values already, into out [n_tokens, heads, 64] (bf16 or fp32); rows in any order."""
+    keys and values already, into out [n_tokens, heads, 64] (bf16 or fp32, not in q's place); rows in any order."""
     dev, T, H = cache.device, batch.n_tokens, q.shape[1]
     fp32 = out.dtype == torch.float32
     _need(batch.device == dev and q.dtype == torch.bfloat16 and (fp32 or out.dtype == torch.bfloat16),
@@ -275,7 +275,7 @@ def saf3r_window_attn_workspace_bytes(layout, window: saf3r_window) -> int:
 
 def saf3r_window_attn(layout, window: saf3r_window, q, k, v, out, workspace, stream=None):
     """Attention with a sliding window of views and sinks over q, k, v [H, N, 64] (bf16) held at once,
-    into out [H, N, 64] (bf16 or fp32)."""
+    into out [H, N, 64] (bf16 or fp32, in none of their places)."""
     if torch is None:
         _load_torch()
     L = _hw.layout_of(layout)

@@ -417,7 +417,7 @@ typedef struct {
     int32_t out_is_fp32;
     const void* q;        /* bf16, n_tokens x n_heads rows of 64 */
     int64_t q_token_stride, q_head_stride;
-    void* out;            /* bf16 or fp32 */
+    void* out;            /* bf16 or fp32; no row of it overlaps one of q, or the cache */
     int64_t out_token_stride, out_head_stride;
 } saf3r_query_rows;
 
@@ -444,7 +444,8 @@ size_t saf3r_window_attn_workspace_bytes(const saf3r_layout* layout, const saf3r
 
 /*
  * Attention over views held at once, q, k, v and out as saf3r_dense_attn, each token seeing what `window`
- * says (view_tokens is usually the layout's V, but need not be).  Workspace as saf3r_kv_attn.
+ * says (view_tokens is usually the layout's V, but need not be).  out overlaps none of the others.  Workspace as
+ * saf3r_kv_attn.
  */
 saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* window, const void* q, const void* k,
                                const void* v, void* out, int out_is_fp32, void* workspace, void* stream);

@@ -153,6 +153,48 @@ def test_append_refuses_a_bad_rope_and_sizes_past_31_bits():
     assert _append_status(max_pages=1 << 26) == hw.ERR_UNSUPPORTED
 
 
+WINDOW = dict(view_tokens=4, window=2, n_sink=4, causal=1)
+QUERIES = dict(n_heads=4, out_is_fp32=0, q=P, q_token_stride=256, q_head_stride=64, out=P + (1 << 20), out_token_stride=256,
+               out_head_stride=64)
+
+
+def _attn_status(workspace=P, **kw):
+    c, b, w, r = dict(CACHE), dict(BATCH), dict(WINDOW), dict(QUERIES)
+    for k, v in kw.items():
+        d, k = (c, k[6:]) if k.startswith("cache_") else (b, k) if k in b else (w, k) if k in w else (r, k)
+        d[k] = v
+    c, b, w, r = st.saf3r_kv_cache(**c), st.saf3r_kv_batch(**b), st.saf3r_window(**w), st.saf3r_query_rows(**r)
+    return hw.lib().saf3r_kv_attn(*(ctypes.byref(x) for x in (c, b, w, r)), workspace, None)
+
+
+@pytest.mark.parametrize("kw", [dict(workspace=None), dict(workspace=P + 8), dict(view_tokens=0), dict(window=-1), dict(n_sink=-1),
+                                dict(n_heads=0), dict(n_heads=3), dict(n_heads=66), dict(q=None), dict(out=None), dict(q=P + 8),
+                                dict(out=P + (1 << 20) + 4), dict(out=P), dict(out=P, out_is_fp32=1), dict(q_token_stride=252),
+                                dict(q_head_stride=0), dict(out_head_stride=32), dict(out_token_stride=128), dict(max_new=9),
+                                dict(cache_page=8), dict(cache_k=None), dict(kv_lens=None)])
+def test_attention_refuses_bad_arguments(kw):
+    assert _attn_status(**kw) == hw.ERR_INVALID
+
+
+def test_attention_of_nothing_returns_before_any_device_work():
+    assert _attn_status(n_seqs=0) == hw.OK
+    assert _attn_status(n_tokens=0, max_new=0, q=None, out=None) == hw.OK
+
+
+def test_window_attention_refuses_bad_arguments_and_an_output_over_its_inputs():
+    lay = hw.make_layout(S=2, grid_h=3, grid_w=3, H=2, n_special=1)
+    n = 2 * 2 * 10 * 128  # bytes of a tensor
+
+    def status(q=P, k=P, v=P, out=P + n, fp32=0, ws=P, **kw):
+        w = st.saf3r_window(**{**WINDOW, **kw})
+        return hw.lib().saf3r_window_attn(ctypes.byref(lay), ctypes.byref(w), q, k, v, out, fp32, ws, None)
+
+    for kw in [dict(q=None), dict(k=P + 8), dict(v=None), dict(out=None), dict(ws=None), dict(ws=P + 4), dict(view_tokens=0),
+               dict(window=-1), dict(out=P), dict(out=P + n - 16), dict(out=P - n + 16), dict(out=P - n, fp32=1),
+               dict(k=P + n), dict(v=P + n + 16), dict(v=P + n, fp32=1)]:
+        assert status(**kw) == hw.ERR_INVALID, kw
+
+
 # ------------------------------------------------------------------ checks of the bindings
 
 def _cpu_batch(n=1, t=8):
