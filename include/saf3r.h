@@ -429,10 +429,11 @@ size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv
  * Attention of each sequence's new tokens to its cached tokens, themselves among them (append first):
  * softmax(q . k / sqrt(64)) over the tokens that `window` lets them see.  Pages without a visible token are not
  * read: the caller may have given them to others.  Up to 64 rows per sequence and kv head (max_new * heads per kv head)
- * take a kernel that splits the keys over the GPU; more the tensor-core kernel.  Weights are rounded once, to bf16 or, over 8-bit
- * caches, to fp16 (where those below 2^-14 of a row's first logits' largest weight lose bits, 2^-25 of it at most); sums
- * are in fp32.  What a masked token holds never reaches a row: next to one whose values are not finite, and where the
- * value scales of a row's pages are more than 2^22 apart, rows are computed key by key, at a small fraction of the speed.
+ * take a kernel that splits the keys over the GPU; more the tensor-core kernel.  Weights are rounded once, to bf16 (16 bits in
+ * the kernel for up to 64 rows) or, over 8-bit caches, to fp16 (where those below 2^-14 of a row's first logits' largest weight
+ * lose bits, 2^-25 of it at most); sums are in fp32.  What a masked token holds never reaches a row: next to one whose values
+ * are not finite (up to 64 rows over bf16 caches: also at one in sight), and where the value scales of a row's pages are more
+ * than 2^22 apart, rows are computed key by key, at a small fraction of the speed.
  * workspace: DEVICE, 16-byte aligned, saf3r_kv_attn_workspace_bytes bytes, used by one call at a time
  * (also when calls are captured: graphs that share it must not overlap); it needs no start value.
  */

@@ -135,6 +135,47 @@ def test_masked_rows_may_hold_anything(e4m3, new):
     assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("heads,new", [(2, [1, 1]), (4, [9, 3]), (8, [16, 16])])
+def test_few_rows_over_bf16_keep_16_bits_of_a_weight(heads, new):
+    """Weights in two bf16 terms are off by 2^-8 of 2^-8, so nearly all that is left of an fp32 output's error is
+    the logits' (2d) and the exponentials' (2^-22 each, as the sum's), in rows of a few weights as in rows of many."""
+    hw = _hw()
+    c = Paged(hw, 2, 2, 64, 16, False, seed=5)
+    c.step([900, 3], 1.0, seed=1)
+    for i, scale in enumerate((0.25, 2.0)):
+        batch = c.step(new, 1.0, seed=i + 2)
+        T = batch.n_tokens
+        q = (scale * torch.randn((T, heads, 64), device="cuda", generator=torch.Generator("cuda").manual_seed(i))).bfloat16()
+        out = torch.empty((T, heads, 64), device="cuda")
+        win = hw.make_window()
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, heads), dtype=torch.uint8, device="cuda")
+        hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+        hw.saf3r_check()
+        Q, got, t = _np(q), _np(out), 0
+        for b, n in enumerate(new):
+            end, at = int(c.lens[b]), np.arange(n)
+            k, v = (O.cached_rows(x, s, c.table[b], end, c.page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+            for h in range(heads):
+                k1, v1, q1, pos = k[:, h // (heads // 2)], v[:, h // (heads // 2)], Q[t + at, h], end - n + at
+                want, a = (O.attend(q1, k1, x, pos, 1, 0, 0, True) for x in (v1, np.abs(v1)))
+                d = 2.0 ** -18 * (np.abs(q1) @ np.abs(k1).max(0) / 8)[:, None]
+                assert (np.abs(got[t + at, h] - want) <= a * (2.0 ** -16 + 2 * d + 2.0 ** -18)).all(), (scale, b, h)
+            t += n
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("new", [[1], [5], [90]])
+def test_values_in_every_rows_sight_may_be_infinite(e4m3, new):
+    hw = _hw()
+    c = Paged(hw, 1, 2, 64, 10, e4m3, seed=3)
+    c.step([400], 1.0, seed=1)
+    batch = c.step(new, seed=2)
+    _spoil(c, 0, 30, "v", np.inf)  # 8-bit values hold no infinity: not a number
+    q, out = check_step(c, batch, new, 4, (1000, 0, 0, False), torch.float32, q=torch.zeros((4, batch.n_tokens, 64), device="cuda",
+                                                                                          dtype=torch.bfloat16).transpose(0, 1))
+    assert (torch.isnan(out) if e4m3 else out == np.inf).all()
+
+
 def test_pages_out_of_sight_are_not_read():
     """Their table entries may be anything; a page in sight that is not there is reported."""
     hw = _hw()
