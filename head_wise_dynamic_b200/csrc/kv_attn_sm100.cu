@@ -52,8 +52,8 @@ constexpr int kItem = 256;             // rows of an item
 constexpr int kRowBytes = 128;
 constexpr int kBlockBytes = 128 * kRowBytes;  // 128 rows x 64 bf16
 constexpr float kScaleLog2 = 0.18033688011112042f;  // log2(e) / sqrt(64)
-constexpr float kGrow = 1.8446744073709552e19f;  // a row with weights beyond 2^64 goes key by key
-constexpr float kGrowF16 = 32768.f;    // fp16 weights: 2^15
+constexpr float kGrowLog2 = 64.f, kGrow = 1.8446744073709552e19f;  // a row with weights beyond 2^64 goes key by key
+constexpr float kGrowF16Log2 = 15.f, kGrowF16 = 32768.f;           // fp16 weights: 2^15
 // Codes of a piece's largest scale are multiplied by 2^7 (448 * 2^7 is in fp16's range), those of scales down to 2^-22 of it
 // by 2^-15 at least: exact in fp16, subnormal codes too.
 constexpr int kCodeTop = 7, kWild = 22;
@@ -880,7 +880,9 @@ __device__ __forceinline__ uint64_t range_bits(int a, int b) {
 }
 
 // 2^x0, 2^x1 on the FMA pipe: 2^floor(x) p(x - floor(x)), the floor from one addition rounded down;
-// x below -127 gives 0
+// x below -127 gives 0.  From 128 on the exponent field overflows and the result means nothing, not even by its sign: the
+// reference bounds no later logit, so the callers look at the largest x themselves (a clamp of every x here would cost two
+// instructions a pair instead of one).
 __device__ __forceinline__ void exp2_poly2(float x0, float x1, float& e0, float& e1) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   x0 = fmaxf(x0, -127.f);
@@ -936,14 +938,16 @@ __device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool fir
   return __any_sync(0xffffffffu, now == -INFINITY);
 }
 
-// 16 logits against the reference: weights as bf16 pairs, and their sums into rp.
+// 16 logits against the reference: weights as bf16 pairs, their sums into rp, the largest x of the polynomial into top.
 template <bool kF16, uint32_t kPoly, bool kMask>
-__device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t valid, float scale, float add, uint32_t* pk, float (&rp)[4]) {
+__device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t valid, float scale, float add, uint32_t* pk, float (&rp)[4],
+                                          float& top) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     float x0 = __uint_as_float(s[2 * q]), x1 = __uint_as_float(s[2 * q + 1]);
     ffma2(x0, x1, scale, add);
     if ((kPoly >> q) & 1u) {
+      top = max3f(top, x0, x1);
       exp2_poly2(x0, x1, x0, x1);
     } else {
       x0 = fast_exp2(x0);
@@ -958,25 +962,28 @@ __device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t vali
   }
 }
 
-// A row's 64 logits, 16 at a time, the next 16 on their way; the first 16 were asked for into `a`.
+// A row's 64 logits, 16 at a time, the next 16 on their way; the first 16 were asked for into `a`.  Returns the sum of the
+// weights, which holds only where top, the largest x that the polynomial took (-infinity: none), is below 128.
 template <bool kF16, bool kMask>
-__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, uint32_t (&a)[16], uint32_t (&pk)[32]) {
+__device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, uint32_t (&a)[16], uint32_t (&pk)[32],
+                                         float& top) {
   const float add = m == -INFINITY ? 0.f : -m;
   constexpr uint32_t kPoly = kMask ? 0u : kPolyPairs;
   const uint32_t lo = static_cast<uint32_t>(valid), hi = static_cast<uint32_t>(valid >> 32);
   float rp[4] = {0.f, 0.f, 0.f, 0.f};
   uint32_t b[16];
+  top = -INFINITY;
   tmem_wait_ld();
   tmem_ld16(tS + 16, b);
-  weights16<kF16, (kPoly & 0xffu), kMask>(a, lo, qs, add, pk, rp);
+  weights16<kF16, (kPoly & 0xffu), kMask>(a, lo, qs, add, pk, rp, top);
   tmem_wait_ld();
   tmem_ld16(tS + 32, a);
-  weights16<kF16, ((kPoly >> 8) & 0xffu), kMask>(b, lo >> 16, qs, add, pk + 8, rp);
+  weights16<kF16, ((kPoly >> 8) & 0xffu), kMask>(b, lo >> 16, qs, add, pk + 8, rp, top);
   tmem_wait_ld();
   tmem_ld16(tS + 48, b);
-  weights16<kF16, ((kPoly >> 16) & 0xffu), kMask>(a, hi, qs, add, pk + 16, rp);
+  weights16<kF16, ((kPoly >> 16) & 0xffu), kMask>(a, hi, qs, add, pk + 16, rp, top);
   tmem_wait_ld();
-  weights16<kF16, (kPoly >> 24), kMask>(b, hi >> 16, qs, add, pk + 24, rp);
+  weights16<kF16, (kPoly >> 24), kMask>(b, hi >> 16, qs, add, pk + 24, rp, top);
   return (rp[0] + rp[1]) + (rp[2] + rp[3]);
 }
 
@@ -1160,9 +1167,10 @@ __device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSm
 #pragma unroll
         for (int q = 0; q < 32; ++q) pk[q] = 0u;
       } else {
-        const float sum = all ? weights<false, false>(tS, valid, m, kScaleLog2, first16, pk)
-                              : weights<false, true>(tS, valid, m, kScaleLog2, first16, pk);
-        if (sum > kGrow) flags |= 2;
+        float top;
+        const float sum = all ? weights<false, false>(tS, valid, m, kScaleLog2, first16, pk, top)
+                              : weights<false, true>(tS, valid, m, kScaleLog2, first16, pk, top);
+        if (sum > kGrow || top > kGrowLog2) flags |= 2;
         l += sum;
       }
       tmem_st32(tS, pk);
@@ -1273,14 +1281,15 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       } else {
         const bool first = blk == blk0;
         bool raise = first || unset;
-        float sum;
+        float sum, top;
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
           if (raise) unset = new_reference(tS, tO + h * 64, first, valid, qs, m, l);
           uint32_t first16[16];
           tmem_ld16(tS, first16);
-          sum = all ? weights<kF16, false>(tS, valid, m, qs, first16, pk) : weights<kF16, true>(tS, valid, m, qs, first16, pk);
-          raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)));  // far above the reference, or not a number
+          sum = all ? weights<kF16, false>(tS, valid, m, qs, first16, pk, top) : weights<kF16, true>(tS, valid, m, qs, first16, pk, top);
+          // far above the reference, or not a number
+          raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)) || top > (kF16 ? kGrowF16Log2 : kGrowLog2));
           if (!raise || pass == 1) break;
         }
         l += sum;

@@ -1,0 +1,58 @@
+"""Streaming attention where single keys, values or pages are far from the others.
+
+Tolerances are those of check_rows, written out at the head of test_gpu_streaming_attn.py.
+"""
+import numpy as np
+import pytest
+
+from test_gpu_streaming import Paged, _hw, _np
+from test_gpu_streaming_attn import check_rows, check_step
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+ALL = (1, 0, 0, False)  # every row sees every key
+
+
+def _loud_rows(rows, key):
+    """Query rows [rows, 1, 64] whose logits at a key of `key` in its first dim (0 at keys without one) go from 60 to 2000."""
+    q = torch.zeros((rows, 1, 64), device="cuda")
+    q[:, 0, 0] = 8.0 / key * 60.0 * (2000.0 / 60.0) ** (torch.arange(rows, device="cuda") / (rows - 1))
+    return q.bfloat16()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("block", [1, 4])
+def test_one_key_far_above_the_rest_of_its_row(e4m3, block):
+    """Whatever its place among the 16 keys of a group, and however far above the row's first block its logit is."""
+    hw = _hw()
+    rows, old = 130, 500
+    for at in range(16):
+        c = Paged(hw, 1, 1, 64, 12, e4m3, seed=3)
+        g = torch.Generator(device="cuda").manual_seed(at)
+        kv = torch.randn((old + rows, 2, 1, 64), device="cuda", generator=g)
+        kv[:, 0] = 0.0
+        kv[128 * block + 32 + at, 0, 0, 0] = 16.0
+        kv = kv.bfloat16()
+        c.step([old], k=kv[:old, 0], v=kv[:old, 1])
+        batch = c.step([rows], k=kv[old:, 0], v=kv[old:, 1])
+        check_step(c, batch, [rows], 1, ALL, torch.float32, q=_loud_rows(rows, 16.0))
+
+
+def test_window_attention_with_one_key_far_above_the_rest():
+    hw = _hw()
+    L = hw.make_layout(4, 10, H=1)
+    V, N = 105, 420
+    win = hw.make_window(V, 0, 0, False)
+    ws = torch.empty(hw.saf3r_window_attn_workspace_bytes(L, win), dtype=torch.uint8, device="cuda")
+    q = _loud_rows(N, 16.0).transpose(0, 1).contiguous()
+    for at in range(16):
+        g = torch.Generator(device="cuda").manual_seed(at)
+        v = torch.randn((1, N, 64), device="cuda", generator=g).bfloat16()
+        k = torch.zeros_like(v)
+        k[0, 272 + at, 0] = 16.0
+        out = torch.empty((1, N, 64), device="cuda")
+        hw.saf3r_window_attn(L, win, q, k, v, out, ws)
+        hw.saf3r_check()
+        idx = np.arange(0, N, 3)
+        check_rows(_np(out[0])[idx], _np(q[0])[idx], _np(k[0]), _np(v[0]), idx, (V, 0, 0, False), False, False, f"key {at}")
