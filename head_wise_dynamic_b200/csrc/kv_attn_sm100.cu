@@ -880,9 +880,9 @@ __device__ __forceinline__ uint64_t range_bits(int a, int b) {
 }
 
 // 2^x0, 2^x1 on the FMA pipe: 2^floor(x) p(x - floor(x)), the floor from one addition rounded down;
-// x below -127 gives 0.  From 128 on the exponent field overflows and the result means nothing, not even by its sign: the
-// reference bounds no later logit, so the callers look at the largest x themselves (a clamp of every x here would cost two
-// instructions a pair instead of one).
+// x below -127 gives 0.  From 128 on the exponent field overflows and the result means nothing, not even by its sign, and
+// not a number gives 0: the reference bounds no later logit, so the callers look at the largest x themselves (clamping every
+// x here and letting NaN through would cost several instructions a pair instead of one).
 __device__ __forceinline__ void exp2_poly2(float x0, float x1, float& e0, float& e1) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   x0 = fmaxf(x0, -127.f);
@@ -938,6 +938,13 @@ __device__ __forceinline__ bool new_reference(uint32_t tS, uint32_t tO, bool fir
   return __any_sync(0xffffffffu, now == -INFINITY);
 }
 
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 16 logits against the reference: weights as bf16 pairs, their sums into rp, the largest x of the polynomial into top.
 template <bool kF16, uint32_t kPoly, bool kMask>
 __device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t valid, float scale, float add, uint32_t* pk, float (&rp)[4],
@@ -947,7 +954,7 @@ __device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t vali
     float x0 = __uint_as_float(s[2 * q]), x1 = __uint_as_float(s[2 * q + 1]);
     ffma2(x0, x1, scale, add);
     if ((kPoly >> q) & 1u) {
-      top = max3f(top, x0, x1);
+      top = max3_nan(top, x0, x1);
       exp2_poly2(x0, x1, x0, x1);
     } else {
       x0 = fast_exp2(x0);
@@ -963,7 +970,8 @@ __device__ __forceinline__ void weights16(const uint32_t (&s)[16], uint32_t vali
 }
 
 // A row's 64 logits, 16 at a time, the next 16 on their way; the first 16 were asked for into `a`.  Returns the sum of the
-// weights, which holds only where top, the largest x that the polynomial took (-infinity: none), is below 128.
+// weights, which holds only where top, the largest x that the polynomial took (-infinity: none; NaN if one was), is
+// below 128.
 template <bool kF16, bool kMask>
 __device__ __forceinline__ float weights(uint32_t tS, uint64_t valid, float m, float qs, uint32_t (&a)[16], uint32_t (&pk)[32],
                                          float& top) {
@@ -1171,7 +1179,7 @@ __device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSm
         const float sum = all ? weights<false, false>(tS, valid, m, kScaleLog2, first16, pk, top)
                               : weights<false, true>(tS, valid, m, kScaleLog2, first16, pk, top);
         if (sum > kGrow || top > kGrowLog2) flags |= 2;
-        l += sum;
+        l += top == top ? sum : top;
       }
       tmem_st32(tS, pk);
       tmem_wait_st();
@@ -1292,7 +1300,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
           raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)) || top > (kF16 ? kGrowF16Log2 : kGrowLog2));
           if (!raise || pass == 1) break;
         }
-        l += sum;
+        l += top == top ? sum : top;
       }
       tmem_st32(tS, pk);
       tmem_wait_st();

@@ -56,3 +56,28 @@ def test_window_attention_with_one_key_far_above_the_rest():
         hw.saf3r_check()
         idx = np.arange(0, N, 3)
         check_rows(_np(out[0])[idx], _np(q[0])[idx], _np(k[0]), _np(v[0]), idx, (V, 0, 0, False), False, False, f"key {at}")
+
+
+@pytest.mark.parametrize("over", ["bf16 cache", "8-bit cache", "views"])
+def test_a_key_in_sight_that_is_not_a_number_is_seen_at_every_place(over):
+    """Its values are finite: the rows learn of it by their weights alone."""
+    hw = _hw()
+    L = hw.make_layout(4, 10, H=1)
+    N = 420
+    for at in range(16):
+        g = torch.Generator(device="cuda").manual_seed(at)
+        q, k, v = torch.randn((3, N, 1, 64), device="cuda", generator=g).bfloat16()
+        k[272 + at] = float("nan")
+        out = torch.zeros((N, 1, 64), device="cuda")
+        if over == "views":
+            win = hw.make_window(105, 0, 0, False)
+            ws = torch.empty(hw.saf3r_window_attn_workspace_bytes(L, win), dtype=torch.uint8, device="cuda")
+            hw.saf3r_window_attn(L, win, *(t.transpose(0, 1).contiguous() for t in (q, k, v)), out.view(1, N, 64), ws)
+        else:
+            c = Paged(hw, 1, 1, 64, 7, over == "8-bit cache", seed=3)
+            batch = c.step([N], k=k, v=v)
+            win = hw.make_window(*ALL)
+            ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, 1), dtype=torch.uint8, device="cuda")
+            hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+        hw.saf3r_check()
+        assert torch.isnan(out).all(), at
