@@ -12,8 +12,8 @@
 //          core reads, a TMA box for each page (or 64 rows of it).  Value rows that no row of the item sees are cleared:
 //          what lies behind a sequence's end need not be finite.  bf16: TMA writes the stage itself.  8-bit: the
 //          codes land beside it, and four more warps (4-7) turn them into fp16 times their page's scale over the
-//          largest of the piece: exact where the scales are within 2^22 of one another; where the values' are not, the
-//          piece's rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
+//          largest of the piece: exact where the scales are within 2^22 of one another; where the values' are not, or
+//          the keys' and it would show, the piece's rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
 //   2-3    issue the products, a warp for each tile.
 //   last 16 softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
 //          Sixteen warps, four for each scheduler in different steps, hide each other's waits.
@@ -57,6 +57,10 @@ constexpr float kGrowF16Log2 = 15.f, kGrowF16 = 32768.f;           // fp16 weigh
 // Codes of a piece's largest scale are multiplied by 2^7 (448 * 2^7 is in fp16's range), those of scales down to 2^-22 of it
 // by 2^-15 at least: exact in fp16, subnormal codes too.
 constexpr int kCodeTop = 7, kWild = 22;
+// Keys of scales below that lose up to 448 * 2^-25 (f16_power is 0 from 2^-32 on), queries are below 2: a sum of 64 products is
+// off by 2^-9.2 at most, a logit by that times what the sum is multiplied by.  Up to 2^-3 it is 2^-12, within the exponentials'
+// own error; above (the row's largest query times the largest key beyond about 2^15) the row goes key by key.
+constexpr float kQuiet = 0.125f;
 constexpr int kMaxShares = 160;        // CTAs of a launch at most (one for each SM)
 constexpr int kPlanEntries = 1024;
 // Cost of a key block of two tiles and of one (which waits more), and of an item's start and end, in sixteenths of the first.
@@ -139,7 +143,8 @@ __host__ __device__ __forceinline__ long long share_start(long long each, int ex
 struct alignas(16) BlockScale {
   float of[16];
 };
-// 8-bit: exponents of the largest scales of a piece's keys and values, and whether some value scale is too small beside them.
+// 8-bit: exponents of the largest scales of a piece's keys and values, and whether some scale is too small beside them (1: of
+// the values, 2: of the keys).
 struct PieceScale {
   int k, v, wild;
 };
@@ -537,15 +542,15 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// 8-bit, warp 1: the largest scales of every piece.  Keys of far smaller scales may lose bits: 2^-41 of the largest key at
-// most, which no logit shows.  Values may not, as a row may see them alone.  A scale of 2^-100 is that of rows of zeros (or of
-// values below 2^-91): it does not count as too small.
+// 8-bit, warp 1: the largest scales of every piece, and whether some are too small beside them.  Values may lose no bits,
+// as a row may see such a page alone.  Keys may where no row can tell (kQuiet).  A scale of 2^-100 is that of rows of zeros
+// (or of numbers below 2^-91): it does not count as too small.
 __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, int lane) {
   const KvView& kv = p.kv;
   Feed feed;
   while (const Piece* next = feed.next(p, sm)) {
     const Piece& pc = *next;
-    int k_hi = -127, v_hi = -127, v_lo = 127;
+    int k_hi = -127, k_lo = 127, v_hi = -127, v_lo = 127;
     const int per_log2 = 7 - p.box_log2;  // boxes of a block
     // eight boxes of a lane at a time: their entries, then their scales
     for (int i0 = (pc.blk0 << per_log2) + lane; i0 < (pc.blk1 << per_log2); i0 += 256) {
@@ -559,7 +564,7 @@ __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, i
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const int i = i0 + 32 * c, row = box_row(p, pc, i >> per_log2, i & ((1 << per_log2) - 1), id[c]);
-        ks[c] = vs[c] = 0.f;
+        ks[c] = vs[c] = 0.f;  // exponent -127: does not count
         if (row >= 0) {
           ks[c] = kv.k_scale[row >> kv.page_log2];
           vs[c] = kv.v_scale[row >> kv.page_log2];
@@ -570,14 +575,16 @@ __device__ __forceinline__ void scan_role(const KvAttnParams& p, AttnSmem& sm, i
         const int k = exponent(ks[c]), v = exponent(vs[c]);
         k_hi = max(k_hi, k);
         v_hi = max(v_hi, v);
+        if (k > -100) k_lo = min(k_lo, k);
         if (v > -100) v_lo = min(v_lo, v);
       }
     }
     k_hi = __reduce_max_sync(0xffffffffu, k_hi);
+    k_lo = __reduce_min_sync(0xffffffffu, k_lo);
     v_hi = __reduce_max_sync(0xffffffffu, v_hi);
     v_lo = __reduce_min_sync(0xffffffffu, v_lo);
     if (lane == 0) {
-      sm.piece_scale[feed.i % kPieces] = PieceScale{k_hi, v_hi, v_lo < v_hi - kWild};
+      sm.piece_scale[feed.i % kPieces] = PieceScale{k_hi, v_hi, (v_lo < v_hi - kWild ? 1 : 0) | (k_lo < k_hi - kWild ? 2 : 0)};
       mbar_arrive(&sm.scale_full[feed.i % kPieces]);
     }
     feed.done(sm, lane);
@@ -1323,7 +1330,8 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     const float2 other = sm.stats[par][t][h ^ 1][r];
     const float mo = other.x, lo = fabsf(other.y);
     part |= other.y < 0.f;
-    const bool wild = kF16 && sm.piece_scale[slot].wild != 0;
+    const int wild_scales = sm.piece_scale[slot].wild;
+    const bool wild = kF16 && ((wild_scales & 1) || ((wild_scales & 2) && qs > kQuiet));
     const float mm = fmaxf(m, mo);
     const float fm = m == -INFINITY ? 0.f : fast_exp2(m - mm), fo = mo == -INFINITY ? 0.f : fast_exp2(mo - mm);
     const float den = l * fm + lo * fo;

@@ -5,6 +5,7 @@ Tolerances are those of check_rows, written out at the head of test_gpu_streamin
 import numpy as np
 import pytest
 
+from oracle import streaming as O
 from test_gpu_streaming import Paged, _hw, _np
 from test_gpu_streaming_attn import check_rows, check_step
 
@@ -81,3 +82,53 @@ def test_a_key_in_sight_that_is_not_a_number_is_seen_at_every_place(over):
             hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
         hw.saf3r_check()
         assert torch.isnan(out).all(), at
+
+
+def _check_by_own_keys(c, batch, new, heads, mask, q, rows):
+    """Rows `rows` of the step's only sequence, with a tolerance from the keys that count in each: a logit summed in fp32 is off
+    by 2^-18 of sum |q_d k_d| / 8 (d) and moves weights and sum by 2d, whatever other keys hold; weights in fp16, their
+    exponentials and sums 2^-11 + 2^-12, and n 2^-24 of the largest value in sight."""
+    hw = _hw()
+    out = torch.empty(q.shape, device="cuda")
+    win = hw.make_window(*mask)
+    ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, heads), dtype=torch.uint8, device="cuda")
+    hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+    hw.saf3r_check()
+    end = int(c.lens[0])
+    k, v = (O.cached_rows(x, s, c.table[0], end, c.page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+    for h in range(heads):
+        for r in rows:
+            p, k1, v1, q1 = end - new + r, k[:, h // (heads // c.heads)], v[:, h // (heads // c.heads)], _np(q[r, h])
+            j = O.seen(p, end, *mask)
+            s = k1[j] @ q1 / 8
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            far = w > 1e-30
+            d = 2.0 ** -18 * (np.abs(k1[j][far]) @ np.abs(q1)).max() / 8
+            tol = (w @ np.abs(v1[j])) * (2.0 ** -11 + 2.0 ** -12 + 2 * d) + j.sum() * 2.0 ** -24 * np.abs(v1[j]).max()
+            err = np.abs(_np(out[r, h]) - w @ v1[j])
+            assert (err <= tol).all(), (h, r, err.max(), (err / tol).max())
+
+
+@pytest.mark.parametrize("new", [9, 150])
+@pytest.mark.parametrize("spread", [30, 45, 80])
+@pytest.mark.parametrize("negative", [False, True])
+def test_8bit_keys_of_far_apart_scales(new, spread, negative):
+    """A page of huge keys out of a row's window, or one whose logits are far below the others, leaves the other keys' bits alone."""
+    hw = _hw()
+    c = Paged(hw, 1, 2, 16, 44, True, seed=3)
+    for i in range(2):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        kv = torch.randn(((500, new)[i], 2, 2, 64), device="cuda", generator=g)
+        if i == 0:
+            kv[464:480, 0] = (-kv[464:480, 0].abs() if negative else kv[464:480, 0]) * 2.0 ** spread
+            kv[448:464, 0] = 0.0  # a page of zeros beside it
+        kv = kv.bfloat16()
+        batch = c.step([len(kv)], k=kv[:, 0], v=kv[:, 1])
+    q = torch.randn((new, 4, 64), device="cuda", generator=g)
+    q = (q.abs() if negative else q).bfloat16()
+    if negative:
+        _check_by_own_keys(c, batch, new, 4, (1, 0, 0, True), q, range(0, new, max(1, new // 9)))
+    # of 150 rows with a window of 50 those from 29 on no longer see the page, of 9 with a window of 12 none does
+    window = 50 if new > 29 else 12
+    _check_by_own_keys(c, batch, new, 4, (1, window, 0, True), q, range(29 if new > 29 else 0, new, max(1, new // 9)))
