@@ -132,3 +132,66 @@ def test_8bit_keys_of_far_apart_scales(new, spread, negative):
     # of 150 rows with a window of 50 those from 29 on no longer see the page, of 9 with a window of 12 none does
     window = 50 if new > 29 else 12
     _check_by_own_keys(c, batch, new, 4, (1, window, 0, True), q, range(29 if new > 29 else 0, new, max(1, new // 9)))
+
+
+def _with_zero_pages(hw, where, magnitude, keys=1024, page=16, heads=2):
+    """An 8-bit cache of one sequence whose value pages `where` are zero, the others of `magnitude`."""
+    c = Paged(hw, 1, heads, page, keys // page + 2, True, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv = torch.randn((keys, 2, heads, 64), device="cuda", generator=g)
+    kv[:, 1] *= magnitude
+    for i in where:
+        kv[i * page:(i + 1) * page, 1] = 0.0
+    kv = kv.bfloat16()
+    c.step([keys], k=kv[:, 0], v=kv[:, 1])
+    return c
+
+
+@pytest.mark.parametrize("where", [[0], [0, 1, 2, 3, 4], [1], [2, 17, 30], [63], list(range(64)), list(range(1, 64)), list(range(63))])
+@pytest.mark.parametrize("magnitude", [2.0 ** -60, 1.0, 2.0 ** 60, 2.0 ** 110])
+@pytest.mark.parametrize("new", [1, 5])
+def test_8bit_pages_of_zero_values(where, magnitude, new):
+    """Their keys count in the sum of the weights, wherever the pages lie; rows that see only them are zero."""
+    hw = _hw()
+    c = _with_zero_pages(hw, where, magnitude)
+    k, v = torch.randn((2, new, 2, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).bfloat16()
+    batch = c.step([new], k=k, v=(v.float() * magnitude).bfloat16())
+    for mask in [(1, 0, 0, True), (1, 60, 20, True)]:
+        check_step(c, batch, [new], 4, mask, torch.float32)
+        check_step(c, batch, [new], 4, mask, torch.float32, q=torch.zeros((new, 4, 64), device="cuda").bfloat16())
+
+
+def test_a_value_that_is_not_a_number_on_a_page_of_zeros():
+    hw = _hw()
+    for first in (0, 9):
+        c = _with_zero_pages(hw, [first], 1.0)
+        c.kv.v[c.table[0, first], :, 3, 5] = torch.full((2,), float("nan"), device="cuda").to(torch.float8_e4m3fn)
+        c.v[c.table[0, first], :, 3, 5] = np.nan
+        batch = c.step([1], seed=4)
+        q, out = check_step(c, batch, [1], 4, (1, 0, 0, True), torch.float32)
+        assert torch.isnan(out[..., 5]).all() and torch.isfinite(out[..., 6:]).all()
+
+
+def test_a_page_of_zero_values_costs_no_more_than_another():
+    """Rows next to it went key by key, 400 times as long; 3 times leaves room for a busy machine."""
+    hw = _hw()
+    times = []
+    for where in ([], [0], [500]):
+        c = _with_zero_pages(hw, where, 1.0, keys=16384)
+        batch = c.step([1], seed=4)
+        q = torch.randn((1, 4, 64), device="cuda").bfloat16()
+        out, win = torch.empty_like(q), hw.make_window()
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, 4), dtype=torch.uint8, device="cuda")
+        best = float("inf")
+        for _ in range(10):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(10):
+                hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 100)
+        hw.saf3r_check()
+        times.append(best)
+    print("us with no page of zeros, the first, one in the middle:", times)
+    assert max(times) < 3 * times[0], times
