@@ -1057,6 +1057,7 @@ __device__ __forceinline__ bool load_query(const KvAttnParams& p, AttnSmem& sm, 
 }
 
 // Columns 32h..32h+31 of a piece's row: to the output, or to the share's slot.  (Run by a whole warp.)
+template <bool kE4m3>
 __device__ __forceinline__ void finish_row(const KvAttnParams& p, const Piece& pc, int row, int h, int tok, float mm, float den, bool part,
                                            bool wild, const float (&o)[32], int lane) {
   if (pc.slot >= 0) {
@@ -1097,7 +1098,7 @@ __device__ __forceinline__ void finish_row(const KvAttnParams& p, const Piece& p
     const int src = __ffs(todo) - 1;
     todo &= todo - 1;
     const int tk = __shfl_sync(0xffffffffu, tok, src), hd = __shfl_sync(0xffffffffu, head, src);
-    exact_row(p, pc.b, pc.s.len, pc.s.row0 + tk, pc.s.len - pc.s.n_new + tk, hd, lane, 32 * h, 32 * h + 32);
+    exact_row<kE4m3>(p, pc.b, pc.s.len, pc.s.row0 + tk, pc.s.len - pc.s.n_new + tk, hd, lane, 32 * h, 32 * h + 32);
   }
 }
 
@@ -1226,7 +1227,7 @@ __device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSm
 #pragma unroll
       for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(x[q]) * scale;
     }
-    finish_row(p, pc, t * 128 + r, h, tok, m, den, (flags & 1) != 0, (flags & 2) != 0, o, lane);
+    finish_row<false>(p, pc, t * 128 + r, h, tok, m, den, (flags & 1) != 0, (flags & 2) != 0, o, lane);
     feed.done(sm, lane);
   }
 }
@@ -1348,7 +1349,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
 #pragma unroll
       for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(oa[q]) * f0 + __uint_as_float(ob[q]) * f1;
     }
-    finish_row(p, pc, t * 128 + r, h, tok, mm, den, part, wild, o, lane);
+    finish_row<kF16>(p, pc, t * 128 + r, h, tok, mm, den, part, wild, o, lane);
     feed.done(sm, lane);
   }
 }
@@ -1446,6 +1447,7 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
 
 // Finishes the items that shares' borders cut: block (i, y) has rows 32y.. of the item first cut by share i's
 // start.  8 threads a row, 8 columns each; pieces in their order.
+template <bool kE4m3>
 __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ KvAttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Work& wk = *reinterpret_cast<const Work*>(p.ws);
@@ -1500,7 +1502,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
   for (int k = 0; k < 4; ++k) {
     if (!((todo >> (8 * k)) & 0xffu)) continue;
     const int tk = __shfl_sync(0xffffffffu, tok, 8 * k), hd = __shfl_sync(0xffffffffu, head, 8 * k);
-    exact_row(p, cut.b, cut.len, cut.first + tk, cut.len - cut.n_new + tk, hd, lane, 0, kD);
+    exact_row<kE4m3>(p, cut.b, cut.len, cut.first + tk, cut.len - cut.n_new + tk, hd, lane, 0, kD);
   }
 }
 
@@ -1549,7 +1551,7 @@ saf3r_status launch_attn(const KvAttnParams& p0, cudaStream_t stream, int* n_lau
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kv_join_kernel, p) != cudaSuccess) return SAF3R_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, p.e4m3 ? kv_join_kernel<true> : kv_join_kernel<false>, p) != cudaSuccess) return SAF3R_ERR_CUDA;
     ++*n_launch;
   }
   return SAF3R_OK;

@@ -244,9 +244,10 @@ __device__ __forceinline__ void store8(const KvAttnParams& p, const Item& it, in
         make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
   }
 }
+template <bool kE4m3>
 __device__ __forceinline__ void exact_item_row(const KvAttnParams& p, const Item& it, int row, int R, int lane) {
   const int i = it.rg * R + row, tok = p.by_group.div(i);
-  exact_row(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i - tok * p.group, lane, 0, kD);
+  exact_row<kE4m3>(p, it.b, it.s.len, it.s.row0 + tok, it.s.len - it.s.n_new + tok, it.hk * p.group + i - tok * p.group, lane, 0, kD);
 }
 
 struct DecodeSmem {
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
           const uint32_t todo = __ballot_sync(0xffffffffu, live && ((bad && part) || wild));
           if (live && !(todo & (0x11111111u << t))) store8(p, it, row, R, 8 * g, x);
           for (int q = 0; q < 4; ++q)
-            if (todo & (0x11111111u << q)) exact_item_row(p, it, 8 * b + 2 * q + c, R, lane);
+            if (todo & (0x11111111u << q)) exact_item_row<kE4m3>(p, it, 8 * b + 2 * q + c, R, lane);
         } else if (live) {
           float4* d = reinterpret_cast<float4*>(&sl->o[row][8 * g]);
           d[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
 // Joins the parts of one item (block x: its kv head and row group, y: its sequence).  Few rows get several warps each, which
 // take parts in turn: their weights first, then 2 columns a lane, in a fixed order.
 constexpr int kJoinWarps = 8;
-template <int kB>
+template <bool kE4m3, int kB>
 __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __grid_constant__ KvAttnParams p) {
   constexpr int R = 8 * kB;
   __shared__ float s_a[kJoinWarps][kD], s_big[kJoinWarps], s_sum[kJoinWarps];
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
     const bool bad = !(fabsf(a0) <= 3.402823466e+38f && fabsf(a1) <= 3.402823466e+38f);
     const int i = rg * R + row, tok = p.by_group.div(i), head = hk * p.group + i - tok * p.group;
     if ((flags & 2) || ((flags & 1) && __any_sync(0xffffffffu, bad))) {
-      exact_row(p, blockIdx.y, s.len, s.row0 + tok, s.len - s.n_new + tok, head, lane, 0, kD);
+      exact_row<kE4m3>(p, blockIdx.y, s.len, s.row0 + tok, s.len - s.n_new + tok, head, lane, 0, kD);
       continue;
     }
     const long long at = (s.row0 + tok) * p.out_ts + head * p.out_hs + 2 * lane;
@@ -805,7 +806,9 @@ saf3r_status launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_l
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, wide ? decode_join_kernel<2> : decode_join_kernel<1>, p) != cudaSuccess) return SAF3R_ERR_CUDA;
+  const auto join = p.e4m3 ? (wide ? decode_join_kernel<true, 2> : decode_join_kernel<true, 1>)
+                           : (wide ? decode_join_kernel<false, 2> : decode_join_kernel<false, 1>);
+  if (cudaLaunchKernelEx(&cfg, join, p) != cudaSuccess) return SAF3R_ERR_CUDA;
   ++*n_launch;
   return SAF3R_OK;
 }

@@ -195,3 +195,45 @@ def test_a_page_of_zero_values_costs_no_more_than_another():
         times.append(best)
     print("us with no page of zeros, the first, one in the middle:", times)
     assert max(times) < 3 * times[0], times
+
+
+def test_rows_that_go_key_by_key_end_before_others_give_up_waiting():
+    """Ten sequences of 4,200 keys whose value scales are too far apart for the products, 64 heads of 70 rows each: a warp's 32
+    rows of an item take less than a wait budget of 25 ms (60 ms at 0.46 us a key), and are right."""
+    hw = _hw()
+    seqs, heads, page, end, new = 10, 64, 64, 4200, 70
+    per = -(-end // page)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv = hw.PagedKV.empty(seqs * per, heads, page, hw.KV_E4M3)
+    for t in (kv.k, kv.v):
+        t.copy_(torch.randn(t.shape, device="cuda", generator=g).to(t.dtype))
+    kv.k_scale.fill_(1.0)
+    kv.v_scale.fill_(1.0)
+    kv.v_scale[3::per] = 2.0 ** 30
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = hw.KVBatch(torch.arange(seqs + 1, **i32) * new, torch.full((seqs,), end, **i32),
+                       torch.arange(seqs * per, **i32).view(seqs, per), seqs * new, new)
+    q = torch.randn((seqs * new, heads, 64), device="cuda", generator=g).bfloat16()
+    out, win = torch.empty(q.shape, device="cuda"), hw.make_window()
+    ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(kv, batch, win, heads), dtype=torch.uint8, device="cuda")
+    hw.saf3r_set_wait_budget(50_000_000)
+    try:
+        hw.saf3r_kv_attn(kv, batch, win, q, out, ws)
+        hw.saf3r_check()
+    finally:
+        hw.saf3r_set_wait_budget(0)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    hw.saf3r_kv_attn(kv, batch, win, q, out, ws)
+    b.record()
+    b.synchronize()
+    hw.saf3r_check()
+    print("us with all rows key by key:", a.elapsed_time(b) * 1000)
+    for s, r, h in [(0, 0, 0), (3, 69, 5), (9, 33, 63), (5, 64, 31), (7, 12, 12)]:
+        pages, n = slice(s * per, (s + 1) * per), end - new + r + 1
+        k = kv.k[pages, h].reshape(-1, 64)[:n].double()
+        v = (kv.v[pages, h].double() * kv.v_scale[pages, h].double()[:, None, None]).reshape(-1, 64)[:n]
+        w = torch.softmax(k @ q[s * new + r, h].double() / 8, 0)
+        # fp32 logits (2^-18 of sum |q k| / 8, twice: weights and sum), exponentials and sums
+        tol = (w @ v.abs()) * (2.0 ** -17 * (k.abs() @ q[s * new + r, h].double().abs()).max() / 8 + 2.0 ** -18)
+        assert ((out[s * new + r, h].double() - w @ v).abs() <= tol).all(), (s, r, h)
