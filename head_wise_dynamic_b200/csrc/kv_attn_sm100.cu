@@ -1074,10 +1074,13 @@ __device__ __forceinline__ void finish_row(const KvAttnParams& p, const Piece& p
   }
   const int a = pc.row0 + min(row, pc.rows - 1), head = pc.hk * p.group + a - tok * p.group;
   const bool live = row < pc.rows;
-  bool bad = false;
+  bool nan = false, inf = false;
 #pragma unroll
-  for (int q = 0; q < 32; ++q) bad |= !(fabsf(o[q]) <= 3.402823466e+38f);
-  bad = (bad && part) || wild;
+  for (int q = 0; q < 32; ++q) {
+    nan |= o[q] != o[q];
+    inf |= fabsf(o[q]) == INFINITY;
+  }
+  const bool bad = (nan && part) || inf || wild;
   if (live && !bad) {
     const long long at = (pc.s.row0 + tok) * p.out_ts + head * p.out_hs + 32 * h;
     if (p.out_fp32) {
@@ -1092,7 +1095,7 @@ __device__ __forceinline__ void finish_row(const KvAttnParams& p, const Piece& p
                           pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
     }
   }
-  // a value out of the row's sight is not finite (or one in sight is): key by key
+  // a value out of the row's sight is not finite, or a sum of weights times values left fp32's range: key by key
   uint32_t todo = __ballot_sync(0xffffffffu, live && bad);
   while (todo) {
     const int src = __ffs(todo) - 1;
@@ -1455,7 +1458,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
   const int r = blockIdx.y * 32 + (threadIdx.x >> 3), col = (threadIdx.x & 7) * 8, lane = threadIdx.x & 31;
   if (!cut.valid || blockIdx.y * 32 >= cut.rows) return;
   float mm = -INFINITY, l = 0.f, o[8];
-  bool part = false, wild = false;
+  bool part = false, wild = false, nan = false;  // nan: in a piece's answer
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
   int b0 = 0;
@@ -1468,6 +1471,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
       const float4* src = reinterpret_cast<const float4*>(&sl.o[r][col]);
       const float4 x = src[0], y = src[1];
       o[0] = o[0] * f + x.x * g; o[1] = o[1] * f + x.y * g; o[2] = o[2] * f + x.z * g; o[3] = o[3] * f + x.w * g;
+      nan |= x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w || y.x != y.x || y.y != y.y || y.z != y.z || y.w != y.w;
       o[4] = o[4] * f + y.x * g; o[5] = o[5] * f + y.y * g; o[6] = o[6] * f + y.z * g; o[7] = o[7] * f + y.w * g;
       l = l * f + g;
       part |= (sl.part[r] & 1) != 0;
@@ -1483,9 +1487,9 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     o[i] *= inv;
     bad |= !(fabsf(o[i]) <= 3.402823466e+38f);
   }
-  // a row is exact as a whole: its 8 threads agree
+  // a row is exact as a whole: its 8 threads agree.  (Not finite though no piece holds a NaN: the sum left fp32's range.)
   const bool live = r < cut.rows;
-  uint32_t todo = __ballot_sync(0xffffffffu, live && ((bad && part) || wild));
+  uint32_t todo = __ballot_sync(0xffffffffu, live && ((bad && (part || !nan)) || wild));
   const bool mine = ((todo >> (lane & 24)) & 0xffu) != 0;
   const int a = cut.row0 + r, tok = p.by_group.div(a), head = cut.hk * p.group + a - tok * p.group;
   if (live && !mine) {

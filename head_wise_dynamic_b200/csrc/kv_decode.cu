@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
   auto slot = [&](int i) -> const Slot& { return base[2LL * i + (i == i0 ? 1 : 0)]; };
   for (int row = warp / turn; row < rows; row += kJoinWarps / turn) {
     float big = -INFINITY, sum = 0.f, a0 = 0.f, a1 = 0.f;
-    int flags = 0;
+    int flags = 0;  // the parts' and, 4: some part's answer is not a number
     for (int i = i0 + at0; i <= i1; i += 32 * turn) {  // 32 parts at a time
       float w = -INFINITY;
       const int mine = i + lane * turn;
@@ -720,6 +720,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
         const float wk = __shfl_sync(0xffffffffu, w, k);
         const float2 x = reinterpret_cast<const float2*>(slot(i + k * turn).o[row])[lane];
         sum += wk;
+        if (x.x != x.x || x.y != x.y) flags |= 4;
         a0 += wk * x.x;
         a1 += wk * x.y;
       }
@@ -752,7 +753,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
     a1 *= inv;
     const bool bad = !(fabsf(a0) <= 3.402823466e+38f && fabsf(a1) <= 3.402823466e+38f);
     const int i = rg * R + row, tok = p.by_group.div(i), head = hk * p.group + i - tok * p.group;
-    if ((flags & 2) || ((flags & 1) && __any_sync(0xffffffffu, bad))) {
+    // not finite though no part holds a NaN: the sum left fp32's range
+    if ((flags & 2) || ((flags & 5) != 4 && __any_sync(0xffffffffu, bad))) {
       exact_row<kE4m3>(p, blockIdx.y, s.len, s.row0 + tok, s.len - s.n_new + tok, head, lane, 0, kD);
       continue;
     }

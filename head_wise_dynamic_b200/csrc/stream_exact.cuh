@@ -96,11 +96,14 @@ static __device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int 
       float ws = w;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, d);
-      l = l * f + ws;
-      a0 *= f;
-      a1 *= f;
+      // (a0, a1) stays the mean of the values so far: a sum of large ones would leave fp32's range
+      const float before = l * f;
+      l = before + ws;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      a0 *= before * inv;
+      a1 *= before * inv;
       m = mn;
-      const float wv = w * vs;
+      const float wv = w * inv * vs;
 #pragma unroll 1
       for (int i0 = 0; i0 < 32; i0 += 4) {
         uint32_t x[4];
@@ -122,9 +125,6 @@ static __device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int 
       }
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  a0 *= inv;
-  a1 *= inv;
   if (2 * lane < c0 || 2 * lane >= c1) return;
   const long long o = row * p.out_ts + head * p.out_hs + 2 * lane;
   if (p.out_fp32) {

@@ -237,3 +237,38 @@ def test_rows_that_go_key_by_key_end_before_others_give_up_waiting():
         # fp32 logits (2^-18 of sum |q k| / 8, twice: weights and sum), exponentials and sums
         tol = (w @ v.abs()) * (2.0 ** -17 * (k.abs() @ q[s * new + r, h].double().abs()).max() / 8 + 2.0 ** -18)
         assert ((out[s * new + r, h].double() - w @ v).abs() <= tol).all(), (s, r, h)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,old,new", [(2, 4000, 1), (2, 4000, 9), (2, 300, 80), (1, 9000, 80), (32, 700, 70)])
+def test_values_next_to_the_largest_number(e4m3, heads, old, new):
+    """Means of values near the end of the range, of one sign and of both, though their sums leave it."""
+    c = Paged(_hw(), 1, heads, 64, 160, e4m3, seed=3)
+    batch = None
+    for i, n in enumerate((old, new)):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        kv = torch.randn((n, 2, heads, 64), device="cuda", generator=g)
+        kv[:, 1, :, :32] = 2.9e38 * (0.5 + 0.5 * torch.rand((n, heads, 32), device="cuda", generator=g))
+        kv[:, 1, :, 32:] = 2.9e38 * torch.sign(kv[:, 1, :, 32:])
+        kv[:, 1, :, 60:] = 1.0
+        kv = kv.bfloat16()
+        batch = c.step([n], k=kv[:, 0], v=kv[:, 1])
+    for mask in [(1, 0, 0, True), (1, 250, 3, True)]:
+        check_step(c, batch, [new], heads, mask, torch.float32, rows=12)
+
+
+def test_window_attention_over_values_next_to_the_largest_number():
+    hw = _hw()
+    L = hw.make_layout(4, 10, H=2)
+    N = 420
+    q, k = torch.randn((2, 2, N, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    v = (3e38 * torch.sign(torch.randn((2, N, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)))).bfloat16()
+    v[..., :32] = v[..., :32].abs()
+    out = torch.empty((2, N, 64), device="cuda")
+    for mask in [(105, 0, 0, False), (105, 2, 0, True)]:
+        win = hw.make_window(*mask)
+        hw.saf3r_window_attn(L, win, q, k, v, out, torch.empty(hw.saf3r_window_attn_workspace_bytes(L, win), dtype=torch.uint8, device="cuda"))
+        hw.saf3r_check()
+        idx = np.arange(0, N, 7)
+        for h in range(2):
+            check_rows(_np(out[h])[idx], _np(q[h])[idx], _np(k[h]), _np(v[h]), idx, mask, False, False, f"head {h}")
