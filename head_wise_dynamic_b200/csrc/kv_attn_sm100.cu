@@ -1220,7 +1220,7 @@ __device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSm
     if (!wait_all(p, sm, &sm.o_done[t], done)) return;
     tc_fence_after();
     flags |= __float_as_int(other.y);
-    const float den = l + other.x, scale = den == 0.f ? 0.f : 1.f / den;
+    const float den = l + other.x, scale = den == 0.f ? (pc.slot >= 0 ? 0.f : no_weight()) : 1.f / den;
     float o[32];
     {
       uint32_t x[32];
@@ -1339,7 +1339,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     const float mm = fmaxf(m, mo);
     const float fm = m == -INFINITY ? 0.f : fast_exp2(m - mm), fo = mo == -INFINITY ? 0.f : fast_exp2(mo - mm);
     const float den = l * fm + lo * fo;
-    float scale = den == 0.f ? 0.f : 1.f / den;
+    float scale = den == 0.f ? (pc.slot >= 0 ? 0.f : no_weight()) : 1.f / den;
     if (kF16) scale *= __uint_as_float(static_cast<uint32_t>(127 + max(sm.piece_scale[slot].v - kCodeTop, -126)) << 23);
     const float f0 = (h ? fo : fm) * scale, f1 = (h ? fm : fo) * scale;
     float o[32];
@@ -1480,7 +1480,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Kv
     }
     b0 = b1;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? no_weight() : 1.f / l;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
         float sum = l[b][c];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? (only ? no_weight() : 0.f) : 1.f / sum;
         float x[8];
         bool bad = false;
 #pragma unroll
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
         flags |= s_flags[warp + q];
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? no_weight() : 1.f / sum;
     a0 *= inv;
     a1 *= inv;
     const bool bad = !(fabsf(a0) <= 3.402823466e+38f && fabsf(a1) <= 3.402823466e+38f);

@@ -21,6 +21,10 @@ __device__ __forceinline__ long long kv_row(const KvAttnParams& p, int id, int h
   return ((*scale << kv.page_log2) + (j & (kv.page - 1))) * kD;
 }
 
+// The answer of a row whose weights add up to 0.  Every row sees itself at least, so all its logits are minus infinity, and
+// the softmax of those is not a number.
+__device__ __forceinline__ float no_weight() { return __uint_as_float(0x7fffffffu); }
+
 // Two neighbouring values (bits of bf16, or codes) as fp32.
 template <bool kCodes>
 __device__ __forceinline__ float2 pair_of(uint32_t bits) {
@@ -125,6 +129,7 @@ static __device__ __noinline__ void exact_row(const KvAttnParams& p, int b, int 
       }
     }
   }
+  if (l == 0.f) a0 = a1 = no_weight();
   if (2 * lane < c0 || 2 * lane >= c1) return;
   const long long o = row * p.out_ts + head * p.out_hs + 2 * lane;
   if (p.out_fp32) {

@@ -272,3 +272,59 @@ def test_window_attention_over_values_next_to_the_largest_number():
         idx = np.arange(0, N, 7)
         for h in range(2):
             check_rows(_np(out[h])[idx], _np(q[h])[idx], _np(k[h]), _np(v[h]), idx, mask, False, False, f"head {h}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,old,new", [(2, 4000, 1), (2, 40, 1), (2, 4000, 9), (2, 300, 80), (1, 9000, 80), (32, 200, 70)])
+def test_rows_of_infinite_logits(e4m3, heads, old, new):
+    """Minus infinity at every key (as at any with plus infinity) is not a number; the rows beside such a one are as always."""
+    hw = _hw()
+    c = Paged(hw, 1, heads, 64, 160, e4m3, seed=3)
+    for i, n in enumerate((old, new)):
+        kv = torch.randn((n, 2, heads, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))
+        kv[:, 0, :, 0] = 0.5 + kv[:, 0, :, 0].abs()
+        kv = kv.bfloat16()
+        batch = c.step([n], k=kv[:, 0], v=kv[:, 1])
+    for value in (-float("inf"), float("inf")):
+        q = torch.randn((new, heads, 64), device="cuda").bfloat16()
+        q[new // 2:, :, 0] = value
+        for mask in [(1, 0, 0, True), (1, 250, 3, True)]:
+            out = torch.zeros(q.shape, device="cuda")
+            win = hw.make_window(*mask)
+            ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, heads), dtype=torch.uint8, device="cuda")
+            hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+            hw.saf3r_check()
+            assert torch.isfinite(out[:new // 2]).all() and torch.isnan(out[new // 2:]).all(), (value, mask)
+
+
+@pytest.mark.parametrize("new", [1, 9, 80])
+def test_a_key_of_minus_infinity_takes_no_part(new):
+    hw = _hw()
+    c = Paged(hw, 1, 2, 64, 12, False, seed=3)
+    batch = None
+    for i, n in enumerate((500, new)):
+        kv = torch.randn((n, 2, 2, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(i))
+        if i == 0:
+            kv[:16, 0, :, 0] = -float("inf")  # at every place of a group, and first in a row's first block
+            kv[296:300, 0, :, 0] = -float("inf")
+        kv = kv.bfloat16()
+        batch = c.step([n], k=kv[:, 0], v=kv[:, 1])
+    q = torch.randn((new, 4, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    q[..., 0] = q[..., 0].abs() + 0.1
+    q = q.bfloat16()
+    out = torch.empty(q.shape, device="cuda")
+    for mask in [(1, 0, 0, True), (1, 1000, 0, False), (1, 250, 8, True)]:
+        win = hw.make_window(*mask)
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, 4), dtype=torch.uint8, device="cuda")
+        hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+        hw.saf3r_check()
+        k, v = (O.cached_rows(x, None, c.table[0], 500 + new, 64) for x in (c.k, c.v))
+        far = np.where(np.isinf(k), 0.0, k)  # for the tolerance
+        for h in range(4):
+            for r in range(0, new, 7):
+                j = O.seen(500 + r, 500 + new, *mask)
+                s = k[j, h // 2] @ _np(q[r, h]) / 8
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                tol = (w @ np.abs(v[j, h // 2])) * (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -17 * (np.abs(far[j, h // 2]) @ np.abs(_np(q[r, h]))).max() / 8)
+                assert (np.abs(_np(out[r, h]) - w @ v[j, h // 2]) <= tol).all(), (mask, h, r)
