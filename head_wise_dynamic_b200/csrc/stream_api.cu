@@ -21,7 +21,7 @@ bool strides_ok(long long tokens, long long ts, long long heads, long long hs, b
   if ((tokens > 1 && ts < kD) || (heads > 1 && hs < kD)) return false;
   if (tokens > 1 && heads > 1) {
     // rows apart: one dim lies inside the other's step
-    const bool token_major = ts >= (heads - 1) * hs + kD, head_major = hs >= (tokens - 1) * ts + kD;
+    const bool token_major = ts >= (heads - 1) * hs + kD, head_major = hs >= static_cast<__int128>(tokens - 1) * ts + kD;
     if (!token_major && !head_major) return false;
   }
   return true;
@@ -30,6 +30,47 @@ bool strides_ok(long long tokens, long long ts, long long heads, long long hs, b
 bool apart(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x + na <= y || y + nb <= x;
+}
+
+// The rows of a tensor, in bytes.
+struct Rows {
+  long long base, tokens, ts, heads, hs, row;
+  Rows(const void* p, long long tokens_, long long ts_, long long heads_, long long hs_, bool fp32)
+      : base(static_cast<long long>(reinterpret_cast<uintptr_t>(p))),
+        tokens(ts_ ? tokens_ : 1), ts(ts_ * (fp32 ? 4 : 2)), heads(hs_ ? heads_ : 1), hs(hs_ * (fp32 ? 4 : 2)), row(kD * (fp32 ? 4 : 2)) {}
+  __int128 end() const { return static_cast<__int128>(tokens - 1) * ts + static_cast<__int128>(heads - 1) * hs + base + row; }
+};
+
+// Whether a row at distance d + i * step from another one, for some i in lo..hi, shares a byte with it.
+bool row_meets(__int128 d, long long step, long long lo, long long hi, long long row, long long other) {
+  if (lo == hi) return d + static_cast<__int128>(lo) * step < other && d + static_cast<__int128>(lo) * step > -row;
+  const __int128 n = other - 1 - d;
+  __int128 i = n / step - (n % step < 0 ? 1 : 0);  // the last that begins before the other's end
+  if (i > hi) i = hi;
+  return i >= lo && d + i * step > -row;
+}
+
+// Whether a row of a and one of b share a byte.  Ranges that lie apart do not; rows of one packed buffer may interleave.  Where
+// the ranges interleave with unequal token strides, or with more than 2^16 pairs of heads of unequal strides, the answer is yes.
+bool rows_meet(Rows a, Rows b) {
+  if (a.end() <= b.base || b.end() <= a.base) return false;
+  if (a.tokens == 1) a.ts = b.ts;
+  if (b.tokens == 1) b.ts = a.ts;
+  if (a.heads == 1) a.hs = b.hs;
+  if (b.heads == 1) b.hs = a.hs;
+  if (a.ts != b.ts) return true;
+  const __int128 d = static_cast<__int128>(a.base) - b.base;
+  if (a.hs == b.hs) {
+    for (long long i = 1 - b.heads; i < a.heads; ++i)
+      if (row_meets(d + static_cast<__int128>(i) * a.hs, a.ts, 1 - b.tokens, a.tokens - 1, a.row, b.row)) return true;
+    return false;
+  }
+  if (a.heads * b.heads > 65536) return true;
+  for (long long i = 0; i < a.heads; ++i)
+    for (long long j = 0; j < b.heads; ++j)
+      if (row_meets(d + static_cast<__int128>(i) * a.hs - static_cast<__int128>(j) * b.hs, a.ts, 1 - b.tokens, a.tokens - 1, a.row, b.row))
+        return true;
+  return false;
 }
 
 saf3r_status check_cache(const saf3r_kv_cache* c, bool pointers) {
@@ -45,6 +86,17 @@ saf3r_status check_cache(const saf3r_kv_cache* c, bool pointers) {
       (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
     return SAF3R_ERR_INVALID;
   return SAF3R_OK;
+}
+
+// Whether the range of the rows runs into the cache's.
+bool meets_pools(const saf3r_kv_cache* c, const Rows& r) {
+  const long long pages = static_cast<long long>(c->n_pages) * c->n_heads, pool = pages * c->page * kD * (c->type == SAF3R_KV_E4M3 ? 1 : 2);
+  auto meets = [&](const void* p, long long bytes) {
+    const long long at = static_cast<long long>(reinterpret_cast<uintptr_t>(p));
+    return r.base < at + bytes && r.end() > at;
+  };
+  return meets(c->k, pool) || meets(c->v, pool) ||
+         (c->type == SAF3R_KV_E4M3 && (meets(c->k_scale, 4 * pages) || meets(c->v_scale, 4 * pages)));
 }
 
 saf3r_status check_batch(const saf3r_kv_cache* c, const saf3r_kv_batch* b, bool pointers) {
@@ -111,8 +163,10 @@ saf3r_status saf3r_rope(const saf3r_rope_cfg* rope, const saf3r_rope_args* a, vo
   if (!strides_ok(a->n_tokens, a->x_token_stride, a->n_heads, a->x_head_stride, a->x_is_fp32 != 0, false) ||
       !strides_ok(a->n_tokens, a->out_token_stride, a->n_heads, a->out_head_stride, a->out_is_fp32 != 0, true))
     return SAF3R_ERR_INVALID;
-  if (a->x == a->out && ((a->x_is_fp32 != 0) != (a->out_is_fp32 != 0) || a->x_token_stride != a->out_token_stride ||
-                         a->x_head_stride != a->out_head_stride))
+  const bool in_place = a->x == a->out && (a->x_is_fp32 != 0) == (a->out_is_fp32 != 0) &&
+                        a->x_token_stride == a->out_token_stride && a->x_head_stride == a->out_head_stride;
+  if (!in_place && rows_meet(Rows(a->x, a->n_tokens, a->x_token_stride, a->n_heads, a->x_head_stride, a->x_is_fp32 != 0),
+                             Rows(a->out, a->n_tokens, a->out_token_stride, a->n_heads, a->out_head_stride, a->out_is_fp32 != 0)))
     return SAF3R_ERR_INVALID;
   int sms = 0, *err = nullptr;
   const saf3r_status st = device(&sms, &err);
@@ -151,6 +205,9 @@ saf3r_status saf3r_kv_append(const saf3r_kv_cache* cache, const saf3r_kv_batch* 
   if (rope && (!rows->pos || (reinterpret_cast<uintptr_t>(rows->pos) & 3))) return SAF3R_ERR_INVALID;
   if (!strides_ok(batch->n_tokens, rows->k_token_stride, cache->n_heads, rows->k_head_stride, false, false) ||
       !strides_ok(batch->n_tokens, rows->v_token_stride, cache->n_heads, rows->v_head_stride, false, false))
+    return SAF3R_ERR_INVALID;
+  if (meets_pools(cache, Rows(rows->k, batch->n_tokens, rows->k_token_stride, cache->n_heads, rows->k_head_stride, false)) ||
+      meets_pools(cache, Rows(rows->v, batch->n_tokens, rows->v_token_stride, cache->n_heads, rows->v_head_stride, false)))
     return SAF3R_ERR_INVALID;
   int sms = 0, *err = nullptr;
   if ((st = device(&sms, &err)) != SAF3R_OK) return st;
@@ -195,12 +252,14 @@ saf3r_status saf3r_kv_attn(const saf3r_kv_cache* cache, const saf3r_kv_batch* ba
   if (batch->n_seqs == 0 || batch->n_tokens == 0 || batch->max_new == 0) return SAF3R_OK;
   if (!rows->q || !rows->out || !workspace || !aligned16(rows->q) || !aligned16(rows->out) || !aligned16(workspace))
     return SAF3R_ERR_INVALID;
-  // a row may be computed again after others of its tile were written, from the queries
-  if (rows->out == rows->q) return SAF3R_ERR_INVALID;
   if (!strides_ok(batch->n_tokens, rows->q_token_stride, rows->n_heads, rows->q_head_stride, false, true) ||
       !strides_ok(batch->n_tokens, rows->out_token_stride, rows->n_heads, rows->out_head_stride, rows->out_is_fp32 != 0,
                   true))
     return SAF3R_ERR_INVALID;
+  // a row may be computed again, from the queries and the cache, after others were written
+  const Rows q(rows->q, batch->n_tokens, rows->q_token_stride, rows->n_heads, rows->q_head_stride, false);
+  const Rows out(rows->out, batch->n_tokens, rows->out_token_stride, rows->n_heads, rows->out_head_stride, rows->out_is_fp32 != 0);
+  if (rows_meet(q, out) || meets_pools(cache, out)) return SAF3R_ERR_INVALID;
   int sms = 0, *err = nullptr;
   if ((st = device(&sms, &err)) != SAF3R_OK) return st;
   KvAttnParams p;

@@ -284,7 +284,9 @@ saf3r_status saf3r_kept_pairs(const saf3r_layout* layout, const saf3r_head_cfg* 
  *
  * Strides are in elements; a row's 64 values are contiguous.  Row starts must be 16-byte aligned
  * (base pointers, and token and head strides a multiple of 8 for bf16 tensors, of 4 for fp32 ones).
- * Strides may be in any order (token-major or head-major), but not negative.
+ * Strides may be in any order (token-major or head-major), but not negative; rows of queries and outputs may not overlap
+ * one another.  Calls whose output shares bytes with what they read are refused (SAF3R_ERR_INVALID), but for rotation in
+ * place.  Rows of one packed buffer may interleave where their token strides are equal (in bytes) or their ranges lie apart.
  */
 
 /* How the rotated dims of a head pair up. */

@@ -328,3 +328,95 @@ def test_a_key_of_minus_infinity_takes_no_part(new):
                 w /= w.sum()
                 tol = (w @ np.abs(v[j, h // 2])) * (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -17 * (np.abs(far[j, h // 2]) @ np.abs(_np(q[r, h]))).max() / 8)
                 assert (np.abs(_np(out[r, h]) - w @ v[j, h // 2]) <= tol).all(), (mask, h, r)
+
+
+def _random_rows(rng, tokens, heads, size, written):
+    """Strides (elements) of rows of 64 in one of the orders; rows that are only read may be repeated."""
+    unit = 16 // size
+    if rng.integers(2):
+        hs = 64 + unit * int(rng.integers(0, 9))
+        ts = (heads - 1) * hs + 64 + unit * int(rng.integers(0, 40))
+    else:
+        ts = 64 + unit * int(rng.integers(0, 9))
+        hs = (tokens - 1) * ts + 64 + unit * int(rng.integers(0, 40))
+    if not written and rng.integers(4) == 0:
+        ts, hs = (0, hs) if rng.integers(2) else (ts, 0)
+    return ts, hs
+
+
+def _units(at, ts, hs, tokens, heads, size):
+    """The 16-byte units of every row."""
+    i = at + (np.arange(tokens)[:, None] * ts + np.arange(heads) * hs) * size // 16
+    return (i[..., None] + np.arange(4 * size)).ravel()
+
+
+def test_rows_of_one_buffer_interleave_or_are_refused():
+    """Rotation between two sets of rows of one buffer, against a count of the bytes that they share."""
+    hw = _hw()
+    rng = np.random.default_rng(1)
+    cfg = hw.make_rope((32, 32))
+    ran = refused = careful = 0
+    for _ in range(1500):
+        T, H = int(rng.integers(1, 6)), int(rng.integers(1, 5))
+        sx, so = (int(rng.choice([2, 4])) for _ in range(2))
+        xt, xh = _random_rows(rng, T, H, sx, False)
+        ot, oh = _random_rows(rng, T, H, so, True)
+        if rng.integers(2):  # one packed buffer: the same steps
+            so, (xt, xh) = sx, _random_rows(rng, T, H, sx, True)
+            gap = 64 * int(rng.integers(1, 4))
+            xt, xh = (xt + gap, xh) if xt > xh else (xt, xh + gap)
+            ot, oh = xt, xh
+        a, b = (int(n) for n in rng.integers(0, 200, 2))
+        ux, uo = _units(a, xt, xh, T, H, sx), _units(b, ot, oh, T, H, so)
+        if sx == so and a == b and (xt if T > 1 else 0, xh if H > 1 else 0) == (ot if T > 1 else 0, oh if H > 1 else 0):
+            continue  # in place
+        buf = torch.randn(int(max(ux.max(), uo.max()) + 8) * 4, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
+        view = lambda n, s, ts, hs: buf.view(torch.float32 if s == 4 else torch.bfloat16).as_strided((T, H, 64), (ts, hs, 1), n * 16 // s)  # noqa: E731
+        if sx == 2 or so == 2:
+            buf = torch.randn(2 * buf.numel(), device="cuda").bfloat16().view(torch.float32)
+        x, out = view(a, sx, xt, xh), view(b, so, ot, oh)
+        pos = torch.randint(0, 40, (T, 2), device="cuda").int()
+        shared = bool(np.intersect1d(ux, uo).size)
+        same_steps = xt * sx == ot * so or T == 1 or xt == 0
+        apart = ux.max() < uo.min() or uo.max() < ux.min()
+        if shared or not (same_steps or apart):
+            with pytest.raises(hw.Saf3rError) as e:
+                hw.saf3r_rope(cfg, x, pos, out)
+            assert e.value.status == hw.ERR_INVALID
+            refused += shared
+            careful += not shared
+            continue
+        ran += not apart
+        want, before = torch.empty((T, H, 64), device="cuda", dtype=out.dtype), buf.clone()
+        hw.saf3r_rope(cfg, x.clone(), pos, want)
+        hw.saf3r_rope(cfg, x, pos, out)
+        assert torch.equal(out.nan_to_num(1e9), want.nan_to_num(1e9))
+        out.zero_()
+        buf2, buf = buf, before
+        view(b, so, ot, oh).zero_()
+        assert torch.equal(buf2.view(torch.int32), buf.view(torch.int32))
+    hw.saf3r_check()
+    assert min(ran, refused) > 50 and careful > 0, (ran, refused, careful)
+
+
+@pytest.mark.parametrize("new", [3, 90])
+def test_queries_and_output_of_one_packed_buffer(new):
+    hw = _hw()
+    c = Paged(hw, 1, 2, 64, 12, False, seed=3)
+    c.step([300], 1.0, seed=1)
+    batch = c.step([new], seed=2)
+    win = hw.make_window(1, 100, 3)
+    ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, 4), dtype=torch.uint8, device="cuda")
+    packed = torch.randn((new, 3, 4, 64), device="cuda").bfloat16()
+    keep, want = packed.clone(), torch.empty((new, 4, 64), device="cuda", dtype=torch.bfloat16)
+    hw.saf3r_kv_attn(c.kv, batch, win, keep[:, 1], want, ws)
+    hw.saf3r_kv_attn(c.kv, batch, win, packed[:, 1], packed[:, 2], ws)
+    keep[:, 2] = want
+    assert torch.equal(packed, keep)
+    rows = packed.view(new, 12, 64)
+    for q, out in [(rows[:, :4], rows[:, 3:7]), (rows[:, 4:8], rows[:, 1:5]), (rows[:-1, :4], rows[1:, 2:6])]:
+        b = batch if len(q) == new else hw.KVBatch(batch.cu_tokens, batch.kv_lens, batch.page_table, new - 1, new - 1)
+        with pytest.raises(hw.Saf3rError) as e:
+            hw.saf3r_kv_attn(c.kv, b, win, q, out, ws)
+        assert e.value.status == hw.ERR_INVALID
+    hw.saf3r_check()
