@@ -106,6 +106,13 @@ __device__ __forceinline__ int scale_exp(float m) {
   return min(max(e - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0), kMinExp), kMaxExp);
 }
 
+// The same in 64 bits (of a magnitude in fp32's range).
+__device__ __forceinline__ int scale_exp(double m) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(m));
+  const int e = static_cast<int>(b >> 52) - 1023;
+  return min(max(e - 8 + ((b & 0xfffffffffffffull) > 0xc000000000000ull ? 1 : 0), kMinExp), kMaxExp);
+}
+
 // Old codes of a page's first `rows` rows, rounded again to a larger scale (f = old scale / new one); `threads` threads.
 __device__ __forceinline__ void rescale_rows(uint8_t* rows_at, int rows, float f, int thread, int threads) {
   uint4* old = reinterpret_cast<uint4*>(rows_at);
@@ -192,6 +199,33 @@ __device__ __forceinline__ void store_turned(uint8_t* row, int o1, int o2, float
   store_codes(row + o2, b, inv);
 }
 
+// Exponent of the scale that turned values of largest magnitude m need.  In fp32 they are off by 2^-21 of |a| + |b|, which is at
+// most twice the larger turned value: where 2^-19 of m could change the exponent, they are turned again in 64 bits (pair0 < 0: these
+// are not turned).  Found for a warp's rows at once: for each thread's it cost 2 us of 15.
+__device__ __forceinline__ bool scale_in_doubt(float m) {
+  return scale_exp(m * (1.f - 1.9073486328125e-06f)) != scale_exp(m * (1.f + 1.9073486328125e-06f));
+}
+template <int N>
+__device__ __noinline__ int exact_scale_exp(const RopeTable& tb, const int32_t* pos, int pair0, const uint16_t* at1, const uint16_t* at2) {
+  Segment<uint16_t, N> u, w;
+  u.load(at1);
+  w.load(at2);
+  double a[N], b[N], s[N], c[N];
+  spread(u, w, a, b);
+  if (pair0 >= 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) rope_sincos(tb, pair0 + i, pos[tb.axis[(pair0 + i) >> 2]], s[i], c[i]);
+    turn(a, b, s, c, tb.interleaved);
+  }
+  double m = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {  // infinities and NaN do not count
+    m = fmax(m, fabs(a[i]) <= kFltMax ? fabs(a[i]) : 0.0);
+    m = fmax(m, fabs(b[i]) <= kFltMax ? fabs(b[i]) : 0.0);
+  }
+  return scale_exp(m);
+}
+
 // Dims of a thread's two segments: those of the rotation, or 2 kSeg neighbours.
 template <int kSeg>
 __device__ __forceinline__ void segments(const RopeTable& tb, bool rope, int g, int& o1, int& o2) {
@@ -213,7 +247,7 @@ template <bool kE4m3, int kSeg>
 __global__ void __launch_bounds__(32 * kWarps, 3) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = 32 / kSeg, kSteps = 16 / kSeg;  // threads of a row; rows of a step are kSeg
   __shared__ Chunk s_chunk;
-  __shared__ float s_amax[2][kWarps];
+  __shared__ int s_exp[2][kWarps];
   extern __shared__ float2 s_sc[];  // [rows of the page][32] (sine, cosine), with a rope
   const KvView& kv = p.kv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -306,14 +340,22 @@ __global__ void __launch_bounds__(32 * kWarps, 3) append_kernel(const __grid_con
         values(st, a, b);
         amax = largest(b, largest(a, amax));
       }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-      if (lane == 0) s_amax[par][warp] = amax;
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // magnitudes order as their bits
+      int e = scale_exp(amax);
+      if (live && is_k && p.has_rope && scale_in_doubt(amax)) {  // the warp's rows once more
+        e = kMinExp;
+        const uint16_t* src = p.k_rows + head * p.k_hs;
+        for (int r = r0; r < r0 + 16; r += kSeg) {
+          if (r < 0 || r >= c.n) continue;
+          const uint16_t* row = src + (c.token + r) * p.k_ts;
+          e = max(e, exact_scale_exp<kSeg>(tb, p.pos + static_cast<long long>(c.token + r) * tb.n_axes, turns ? g * kSeg : -1, row + o1, row + o2));
+        }
+        e = __reduce_max_sync(0xffffffffu, e);
+      }
+      if (lane == 0) s_exp[par][warp] = e;
       __syncthreads();  // also: every thread has read the old scale
       if (live) {
-        float m = 0.f;
-        for (int x = 0; x < team_warps; ++x) m = fmaxf(m, s_amax[par][team * team_warps + x]);
-        const int e = scale_exp(m);
+        for (int x = 0; x < team_warps; ++x) e = max(e, s_exp[par][team * team_warps + x]);
         float to = power_of_two(e), inv = power_of_two(-e);
         uint8_t* dst = (is_k ? kv.k : kv.v) + block * kD;
         if (older) {
@@ -395,10 +437,14 @@ __global__ void __launch_bounds__(32 * kWarps) append_token_kernel(const __grid_
     float* scale = (is_k ? kv.k_scale : kv.v_scale) + (block >> kv.page_log2);
     const bool older = live && r > 0;
     const float was = older ? *scale : 0.f;
-    float m = live ? largest(y, largest(x, 0.f)) : 0.f;
+    const float m = live ? largest(y, largest(x, 0.f)) : 0.f;
+    int e = scale_exp(m);
+    if (turns && live && scale_in_doubt(m)) {
+      const uint16_t* row = p.k_rows + s.row0 * p.k_ts + head * p.k_hs;
+      e = exact_scale_exp<kSeg>(tb, pos, g * kSeg, row + o1, row + o2);
+    }
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const int e = scale_exp(m);
+    for (int d = 1; d < kLanes; d <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, d));
     float now = power_of_two(e), inv = power_of_two(-e);
     const bool grows = older && now > was;
     if (older && !grows) {

@@ -43,9 +43,9 @@ struct Segment {
   }
 };
 
-// The segments' values in fp32.
-template <typename T, int N>
-__device__ __forceinline__ void spread(const Segment<T, N>& u, const Segment<T, N>& w, float (&a)[N], float (&b)[N]) {
+// The segments' values.
+template <typename T, typename V, int N>
+__device__ __forceinline__ void spread(const Segment<T, N>& u, const Segment<T, N>& w, V (&a)[N], V (&b)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     a[i] = u.get(i);
@@ -53,15 +53,16 @@ __device__ __forceinline__ void spread(const Segment<T, N>& u, const Segment<T, 
   }
 }
 
-// Turns the segments' N pairs: (a[i], b[i]), or neighbours inside each segment.  T: what the products are held in.
-template <typename T>
-__device__ __forceinline__ void turn_pair(float& a, float& b, T s, T c) {
+// Turns the segments' N pairs: (a[i], b[i]), or neighbours inside each segment.  T: what the products are held in, V: the
+// values.
+template <typename V, typename T>
+__device__ __forceinline__ void turn_pair(V& a, V& b, T s, T c) {
   const T x = a, y = b;
-  a = static_cast<float>(x * c - y * s);
-  b = static_cast<float>(x * s + y * c);
+  a = static_cast<V>(x * c - y * s);
+  b = static_cast<V>(x * s + y * c);
 }
-template <typename T, int N>
-__device__ __forceinline__ void turn(float (&a)[N], float (&b)[N], const T (&s)[N], const T (&c)[N], bool interleaved) {
+template <typename V, typename T, int N>
+__device__ __forceinline__ void turn(V (&a)[N], V (&b)[N], const T (&s)[N], const T (&c)[N], bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
