@@ -162,7 +162,7 @@ void launch_rope_seg(const RopeParams& p, bool in_fp32, bool out_fp32, dim3 grid
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams& p0, bool in_fp32, bool out_fp32, cudaStream_t stream, int* n_launch) {
+cudaError_t launch_rope(const RopeParams& p0, bool in_fp32, bool out_fp32, int num_sms, cudaStream_t stream, int* n_launch) {
   RopeParams p = p0;
   if (p.n_tokens == 0 || p.n_heads == 0) return cudaSuccess;
   const int seg = p.table.wide ? 8 : 4, tokens = kThreads * seg / 32;
@@ -170,7 +170,7 @@ cudaError_t launch_rope(const RopeParams& p0, bool in_fp32, bool out_fp32, cudaS
   // heads of a block share its sines: as many as leave at least 16 blocks for each SM, and no fewer than are in flight
   const int fly = 64 / (seg * (in_fp32 ? 4 : 2));
   int hpb = 4 * fly;
-  while (hpb > fly && bx * ((p.n_heads + hpb - 1) / hpb) < 16 * 148) hpb /= 2;
+  while (hpb > fly && bx * ((p.n_heads + hpb - 1) / hpb) < 16LL * num_sms) hpb /= 2;
   p.heads_per_block = hpb;
   const dim3 grid(static_cast<unsigned>(bx), (p.n_heads + hpb - 1) / hpb);
   if (seg == 8)

@@ -217,7 +217,7 @@ __device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int po
 #endif
 
 bool build_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t);
-cudaError_t launch_rope(const RopeParams& p, bool in_fp32, bool out_fp32, cudaStream_t stream, int* n_launch);
+cudaError_t launch_rope(const RopeParams& p, bool in_fp32, bool out_fp32, int num_sms, cudaStream_t stream, int* n_launch);
 cudaError_t launch_append(const AppendParams& p, bool e4m3, int num_sms, cudaStream_t stream, int* n_launch);
 
 // few query rows per sequence and kv head (kv_decode.cu)

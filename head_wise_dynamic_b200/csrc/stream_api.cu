@@ -185,7 +185,7 @@ saf3r_status saf3r_rope(const saf3r_rope_cfg* rope, const saf3r_rope_args* a, vo
   p.heads_per_block = 0;
   int launches = 0;
   const cudaError_t e =
-      launch_rope(p, a->x_is_fp32 != 0, a->out_is_fp32 != 0, static_cast<cudaStream_t>(stream), &launches);
+      launch_rope(p, a->x_is_fp32 != 0, a->out_is_fp32 != 0, sms, static_cast<cudaStream_t>(stream), &launches);
   set_launch_count(launches);
   return cuda_status(e);
 }
