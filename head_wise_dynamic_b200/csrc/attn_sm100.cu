@@ -70,8 +70,6 @@ constexpr float kRescaleThreshold = 8.0f;           // log2 units: keep a stale 
 #define SAF3R_POLY_PAIRS 0x80808080u
 #endif
 constexpr uint32_t kPolyPairs = SAF3R_POLY_PAIRS;
-// the cubic of the FMA-pipe exponential: p(f) = 1 + f (c1 + f (c2 + f c3))
-constexpr float kExpC1 = 0.6951168179512024f, kExpC2 = 0.22764486074447632f, kExpC3 = 0.07706713676452637f;
 
 // One 64-row half-block of keys.
 struct Half {
@@ -645,39 +643,6 @@ struct SoftmaxState {
   uint32_t odone_c = 0;
   uint32_t pair_c = 0;
 };
-
-
-// O_t of this warp's key half (64 columns from tO) times alpha: the running max grew by more
-// than the threshold.  O_t already holds the previous blocks' products (s_full of this block
-// was committed after them).
-__device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    uint32_t o[16];
-    tmem_ld16(tO + q * 16, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-    tmem_st16(tO + q * 16, o);
-  }
-}
-
-// 2^x0, 2^x1 on the FMA pipe (see the head of this file).
-__device__ __forceinline__ void exp2_poly2(float x0, float x1, float& e0, float& e1) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: x + kMagic rounded down holds floor(x) in its low bits
-  x0 = fmaxf(x0, -127.f);
-  x1 = fmaxf(x1, -127.f);
-  uint64_t t, xi, f, pp;
-  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(t) : "l"(f32x2(x0, x1)), "l"(f32x2(kMagic, kMagic)));
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(xi) : "l"(t), "l"(f32x2(kMagic, kMagic)));
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(f) : "l"(f32x2(x0, x1)), "l"(xi));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pp) : "l"(f), "l"(f32x2(kExpC3, kExpC3)), "l"(f32x2(kExpC2, kExpC2)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pp) : "l"(pp), "l"(f), "l"(f32x2(kExpC1, kExpC1)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pp) : "l"(pp), "l"(f), "l"(f32x2(1.f, 1.f)));
-  // exponent field += floor(x): (bits of t) << 23 is floor(x) << 23 modulo 2^32
-  e0 = __uint_as_float(static_cast<uint32_t>(pp) + (static_cast<uint32_t>(t) << 23));
-  e1 = __uint_as_float(static_cast<uint32_t>(pp >> 32) + (static_cast<uint32_t>(t >> 32) << 23));
-}
 
 // 2^x0, 2^x1 of pair i of a half-block: on the FMA pipe for the pairs of kPolyPairs, else the SFU.
 __device__ __forceinline__ void exp2_pair(int i, float x0, float x1, float& e0, float& e1) {

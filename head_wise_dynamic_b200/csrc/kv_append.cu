@@ -87,10 +87,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
   float v[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes >> (16 * i))));
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(v[2 * i]), "=f"(v[2 * i + 1]) : "r"(h));
+    const float2 x = f32x2_of_f16x2(f16x2_of_e4m3(codes >> (16 * i)));
+    v[2 * i] = x.x;
+    v[2 * i + 1] = x.y;
   }
   return e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
 }
@@ -128,8 +127,6 @@ __device__ __forceinline__ void rescale_rows(uint8_t* rows_at, int rows, float f
         old[i0 + c * threads] = make_uint4(rescale4(v[c].x, f), rescale4(v[c].y, f), rescale4(v[c].z, f), rescale4(v[c].w, f));
   }
 }
-
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 __device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
   float y[4];

@@ -69,8 +69,6 @@ constexpr int kLeastShare = 2 * kCost2;  // shares smaller than this are not wor
 
 // Pairs (of the 32 of a row's 64 keys) whose exponentials run on the FMA pipe.
 constexpr uint32_t kPolyPairs = 0x10101010u;
-// p(f) = 1 + f (c1 + f (c2 + f c3)), fitted to 2^f on [0, 1) for least maximum relative error (8.6e-5)
-constexpr float kExpC1 = 0.6951168179512024f, kExpC2 = 0.22764486074447632f, kExpC3 = 0.07706713676452637f;
 
 // A share's part of an unfinished item: per row its answer, the sum of its weights and their reference.
 struct Slot {
@@ -518,17 +516,6 @@ __device__ __forceinline__ void side_role(const KvAttnParams& p, AttnSmem& sm, c
   drain();
 }
 
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return h;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 __device__ __forceinline__ int exponent(float scale) { return static_cast<int>((__float_as_uint(scale) >> 23) & 0xffu) - 127; }
 // 2^(kCodeTop + d) twice as fp16 (d <= 0; 0 below fp16's range)
 __device__ __forceinline__ uint32_t f16_power(int d) {
@@ -744,12 +731,11 @@ __device__ __forceinline__ void issue_qk(uint64_t dq, uint64_t dk, uint32_t s_co
 }
 
 // One warp for each tile; the whole warp runs (which keeps the descriptors uniform), one elected lane issues.  A key
-// half goes its own way: as soon as its warps have written P, its O += P V is issued and S = Q K^T of its next 64
+// half goes its own way (8-bit): as soon as its warps have written P, its O += P V is issued and S = Q K^T of its next 64
 // keys behind it, over P.  One product of 128 keys for both halves would read Q from shared memory half as often
 // (tensor time 1024 cycles of a block of 256 rows against 1264), but ties the halves together.
-template <bool kF16>
 __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem_base, int t, int lane) {
-  constexpr int kStages = Ring<kF16>::kStages;
+  constexpr int kStages = Ring<true>::kStages;
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, tmem_base) + t * 256;
   const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[t]), 16, 1024);
   const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
@@ -775,7 +761,7 @@ __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, ui
     if (elect_one()) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        issue_qk<kF16>(q0, k0 + (n % kStages) * kStageDesc + h * (kTileDesc / 2), tmem + h * 64);
+        issue_qk<true>(q0, k0 + (n % kStages) * kStageDesc + h * (kTileDesc / 2), tmem + h * 64);
         mma_commit(&sm.s_full[t][h]);
       }
       if (nblk == 1) mma_commit(&sm.q_empty[t]);
@@ -794,9 +780,9 @@ __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, ui
           const uint32_t s_col = tmem + h * 64, o_col = s_col + 128;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(o_col, s_col + kk * 8, dv + 128 * (4 * h + kk), idesc_of<kF16>(1), j > 0 || kk > 0 ? 1u : 0u);
+            mma_ts(o_col, s_col + kk * 8, dv + 128 * (4 * h + kk), idesc_of<true>(1), j > 0 || kk > 0 ? 1u : 0u);
           if (more) {
-            issue_qk<kF16>(q0, dk + h * (kTileDesc / 2), s_col);
+            issue_qk<true>(q0, dk + h * (kTileDesc / 2), s_col);
             mma_commit(&sm.s_full[t][h]);
           }
           if (h == 1) {
@@ -812,11 +798,10 @@ __device__ __forceinline__ void mma_role(const KvAttnParams& p, AttnSmem& sm, ui
   }
 }
 
-// The same with one accumulator for both key halves of a tile and three S buffers: a step is one key half of
+// bf16: the same with one accumulator for both key halves of a tile and three S buffers: a step is one key half of
 // one block, step n of the tile has buffer n % 3, and a buffer whose P V is issued takes the S of the third step after.
-template <bool kF16>
 __device__ __forceinline__ void mma_role_joint(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem_base, int t, int lane) {
-  constexpr uint32_t kStages = Ring<kF16>::kStages;
+  constexpr uint32_t kStages = Ring<false>::kStages;
   const uint32_t tmem = __reduce_max_sync(0xffffffffu, tmem_base) + t * 256, o_col = tmem + 192;
   const uint64_t q0 = smem_desc_sw128(smem_u32(sm.q[t]), 16, 1024);
   const uint64_t k0 = smem_desc_sw128(smem_u32(sm.ring), 16, 1024);
@@ -844,7 +829,7 @@ __device__ __forceinline__ void mma_role_joint(const KvAttnParams& p, AttnSmem& 
       if (!(i & 1) && !wait_all(p, sm, &sm.full[blk % kStages], (blk / kStages) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
-        issue_qk<kF16>(q0, k0 + (blk % kStages) * kStageDesc + (i & 1) * (kTileDesc / 2), tmem + b * 64);
+        issue_qk<false>(q0, k0 + (blk % kStages) * kStageDesc + (i & 1) * (kTileDesc / 2), tmem + b * 64);
         mma_commit(&sm.s_full[t][b]);
         if (i == steps - 1) mma_commit(&sm.q_empty[t]);
       }
@@ -861,7 +846,7 @@ __device__ __forceinline__ void mma_role_joint(const KvAttnParams& p, AttnSmem& 
         const uint64_t dv = v0 + cs * kStageDesc + 512 * (i & 1);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts(o_col, tmem + buf * 64 + kk * 8, dv + 128 * kk, idesc_of<kF16>(1), i > 0 || kk > 0 ? 1u : 0u);
+          mma_ts(o_col, tmem + buf * 64 + kk * 8, dv + 128 * kk, idesc_of<false>(1), i > 0 || kk > 0 ? 1u : 0u);
         if (i & 1) mma_commit(&sm.empty[cs]);
         if (i == steps - 1) mma_commit(&sm.o_done[t]);
       }
@@ -884,38 +869,6 @@ __device__ __forceinline__ uint64_t range_bits(int a, int b) {
   b = min(b, 64);
   if (a >= b) return 0ull;
   return (~0ull >> (64 - (b - a))) << a;
-}
-
-// 2^x0, 2^x1 on the FMA pipe: 2^floor(x) p(x - floor(x)), the floor from one addition rounded down;
-// x below -127 gives 0.  From 128 on the exponent field overflows and the result means nothing, not even by its sign, and
-// not a number gives 0: the reference bounds no later logit, so the callers look at the largest x themselves (clamping every
-// x here and letting NaN through would cost several instructions a pair instead of one).
-__device__ __forceinline__ void exp2_poly2(float x0, float x1, float& e0, float& e1) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-  x0 = fmaxf(x0, -127.f);
-  x1 = fmaxf(x1, -127.f);
-  uint64_t t, xi, f, pp;
-  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(t) : "l"(f32x2(x0, x1)), "l"(f32x2(kMagic, kMagic)));
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(xi) : "l"(t), "l"(f32x2(kMagic, kMagic)));
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(f) : "l"(f32x2(x0, x1)), "l"(xi));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pp) : "l"(f), "l"(f32x2(kExpC3, kExpC3)), "l"(f32x2(kExpC2, kExpC2)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pp) : "l"(pp), "l"(f), "l"(f32x2(kExpC1, kExpC1)));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(pp) : "l"(pp), "l"(f), "l"(f32x2(1.f, 1.f)));
-  e0 = __uint_as_float(static_cast<uint32_t>(pp) + (static_cast<uint32_t>(t) << 23));
-  e1 = __uint_as_float(static_cast<uint32_t>(pp >> 32) + (static_cast<uint32_t>(t >> 32) << 23));
-}
-
-// O of this warp's rows and key half times alpha
-__device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    uint32_t o[16];
-    tmem_ld16(tO + q * 16, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-    tmem_st16(tO + q * 16, o);
-  }
 }
 
 // Largest logit that a row sees of a chunk.
@@ -1235,7 +1188,7 @@ __device__ __forceinline__ void softmax_role_joint(const KvAttnParams& p, AttnSm
   }
 }
 
-template <bool kF16>
+// 8-bit: a reference and an accumulator for each key half.
 __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm, uint32_t tmem, int sw, int lane) {
   const int t = sw >> 3, h = (sw >> 2) & 1, wq = sw & 3;
   const int r = wq * 32 + lane;  // row of the tile
@@ -1245,7 +1198,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
   Feed feed;
   uint32_t sfull = 0, pieces = 0, n = 0;  // pieces of this tile, key blocks of all
   const Piece* next = feed.next(p, sm);
-  if (next && !load_query<kF16>(p, sm, *next, 0, 0, t, h, r, lane)) return;
+  if (next && !load_query<true>(p, sm, *next, 0, 0, t, h, r, lane)) return;
   while (next) {
     const Piece& pc = *next;
     const uint32_t slot = feed.i % kPieces;
@@ -1254,7 +1207,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       Feed f = feed;
       ++f.i;
       next = f.next(p, sm);
-      return !next || load_query<kF16>(p, sm, *next, pieces, f.i % kPieces, t, h, r, lane);
+      return !next || load_query<true>(p, sm, *next, pieces, f.i % kPieces, t, h, r, lane);
     };
     if (pc.rows <= t * 128) {  // the item has one tile
       n += pc.blk1 - pc.blk0;
@@ -1269,7 +1222,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     bool part = false;  // some streamed key is out of this row's sight
     const Chunks ch = pc.ch;
     const int blk0 = pc.blk0, blk1 = pc.blk1;
-    float qs = kScaleLog2;
+    float qs = 0.f;  // what a product is multiplied by: known once the queries are there
     for (int blk = blk0; blk < blk1; ++blk, ++n) {
       const int i = 2 * blk + h, j0 = ch.key(i);
       const bool have = i < ch.total;
@@ -1287,7 +1240,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
       if (!wait_all(p, sm, &sm.s_full[t][h], sfull & 1)) return;
       ++sfull;
       tc_fence_after();
-      if (kF16 && blk == blk0) {
+      if (blk == blk0) {
         const int e = sm.q_exp[slot][t * 128 + r][h] + sm.piece_scale[slot].k - kCodeTop;
         qs = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + min(max(e, -126), 127)) << 23);
       }
@@ -1306,9 +1259,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
           if (raise) unset = new_reference(tS, tO + h * 64, first, valid, qs, m, l);
           uint32_t first16[16];
           tmem_ld16(tS, first16);
-          sum = all ? weights<kF16, false>(tS, valid, m, qs, first16, pk, top) : weights<kF16, true>(tS, valid, m, qs, first16, pk, top);
+          sum = all ? weights<true, false>(tS, valid, m, qs, first16, pk, top) : weights<true, true>(tS, valid, m, qs, first16, pk, top);
           // far above the reference, or not a number
-          raise = __any_sync(0xffffffffu, !(sum <= (kF16 ? kGrowF16 : kGrow)) || top > (kF16 ? kGrowF16Log2 : kGrowLog2));
+          raise = __any_sync(0xffffffffu, !(sum <= kGrowF16) || top > kGrowF16Log2);
           if (!raise || pass == 1) break;
         }
         l += top == top ? sum : top;
@@ -1335,12 +1288,12 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
     const float mo = other.x, lo = fabsf(other.y);
     part |= other.y < 0.f;
     const int wild_scales = sm.piece_scale[slot].wild;
-    const bool wild = kF16 && ((wild_scales & 1) || ((wild_scales & 2) && qs > kQuiet));
+    const bool wild = (wild_scales & 1) || ((wild_scales & 2) && qs > kQuiet);
     const float mm = fmaxf(m, mo);
     const float fm = m == -INFINITY ? 0.f : fast_exp2(m - mm), fo = mo == -INFINITY ? 0.f : fast_exp2(mo - mm);
     const float den = l * fm + lo * fo;
     float scale = den == 0.f ? (pc.slot >= 0 ? 0.f : no_weight()) : 1.f / den;
-    if (kF16) scale *= __uint_as_float(static_cast<uint32_t>(127 + max(sm.piece_scale[slot].v - kCodeTop, -126)) << 23);
+    scale *= __uint_as_float(static_cast<uint32_t>(127 + max(sm.piece_scale[slot].v - kCodeTop, -126)) << 23);
     const float f0 = (h ? fo : fm) * scale, f1 = (h ? fm : fo) * scale;
     float o[32];
     {
@@ -1352,7 +1305,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnParams& p, AttnSmem& sm
 #pragma unroll
       for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(oa[q]) * f0 + __uint_as_float(ob[q]) * f1;
     }
-    finish_row<kF16>(p, pc, t * 128 + r, h, tok, mm, den, part, wild, o, lane);
+    finish_row<true>(p, pc, t * 128 + r, h, tok, mm, den, part, wild, o, lane);
     feed.done(sm, lane);
   }
 }
@@ -1405,17 +1358,14 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
 
   // registers: launched with 96 x 640 or 80 x 768; 64 x 128 + 104 x 512 and 64 x 256 + 88 x 512 are as many
   if (warp < Ring<kE4m3>::kSoftmax) {
-    if (kE4m3)
-      reg_dealloc_dec<64>();
-    else
-      reg_dealloc_dec<64>();
+    reg_dealloc_dec<64>();
     if (kE4m3 && warp >= 4) {
       convert_role(p, sm, warp - 4, lane);
     } else if (warp >= 2) {
-      if (kE4m3)
-        mma_role<kE4m3>(p, sm, tmem, warp - 2, lane);
+      if constexpr (kE4m3)
+        mma_role(p, sm, tmem, warp - 2, lane);
       else
-        mma_role_joint<kE4m3>(p, sm, tmem, warp - 2, lane);
+        mma_role_joint(p, sm, tmem, warp - 2, lane);
       // also after a wait that gave up: no product is in flight when the block lets its memory go
       if (elect_one()) mma_commit(&sm.drain[warp - 2]);
       __syncwarp();
@@ -1434,8 +1384,8 @@ __global__ void __launch_bounds__(32 * Ring<kE4m3>::kWarps, 1)
       reg_alloc_inc<88>();
     else
       reg_alloc_inc<104>();
-    if (kE4m3)
-      softmax_role<kE4m3>(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
+    if constexpr (kE4m3)
+      softmax_role(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
     else
       softmax_role_joint(p, sm, tmem, warp - Ring<kE4m3>::kSoftmax, lane);
   }
@@ -1545,17 +1495,8 @@ saf3r_status launch_attn(const KvAttnParams& p0, cudaStream_t stream, int* n_lau
   ++*n_launch;
   if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
   if (grid > 1) {
-    // its blocks are set up while the first kernel still runs, and wait for its end on the device
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid - 1, kItem / 32);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, p.e4m3 ? kv_join_kernel<true> : kv_join_kernel<false>, p) != cudaSuccess) return SAF3R_ERR_CUDA;
+    if (launch_behind(p.e4m3 ? kv_join_kernel<true> : kv_join_kernel<false>, dim3(grid - 1, kItem / 32), dim3(256), stream, p) != cudaSuccess)
+      return SAF3R_ERR_CUDA;
     ++*n_launch;
   }
   return SAF3R_OK;

@@ -68,20 +68,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
-  return h;
-}
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // A warp's part of an item that a border cuts: per row the part's answer, log2 of the sum of its weights, and flags.
 struct Slot {
@@ -475,7 +463,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
           const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t a[4] = {f16_of_e4m3(wx[kk]), f16_of_e4m3(wy[kk]), f16_of_e4m3(wx[kk] >> 16), f16_of_e4m3(wy[kk] >> 16)};
+            const uint32_t a[4] = {f16x2_of_e4m3(wx[kk]), f16x2_of_e4m3(wy[kk]), f16x2_of_e4m3(wx[kk] >> 16), f16x2_of_e4m3(wy[kk] >> 16)};
 #pragma unroll
             for (int b = 0; b < kB; ++b) mma_f16(s[b][i], a, qb[b][kk][0], qb[b][kk][1]);
           }
@@ -602,10 +590,10 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm)
           if (kE4m3) {
             const uint32_t sel = (m & 1) ? 0x7362 : 0x5140;
             const uint32_t x = __byte_perm(v[0][m >> 1], v[1][m >> 1], sel), y = __byte_perm(v[2][m >> 1], v[3][m >> 1], sel);
-            a[0] = f16_of_e4m3(x);
-            a[1] = f16_of_e4m3(x >> 16);
-            a[2] = f16_of_e4m3(y);
-            a[3] = f16_of_e4m3(y >> 16);
+            a[0] = f16x2_of_e4m3(x);
+            a[1] = f16x2_of_e4m3(x >> 16);
+            a[2] = f16x2_of_e4m3(y);
+            a[3] = f16x2_of_e4m3(y >> 16);
           } else {
             const int w = kE4m3 ? 0 : m;
             a[0] = __byte_perm(v[0][w], v[1][w], 0x5410);
@@ -797,20 +785,11 @@ saf3r_status launch_decode(const KvAttnParams& p0, cudaStream_t stream, int* n_l
   kernel<<<grid, 32 * kWarps, smem, stream>>>(p, mk, mv);
   ++*n_launch;
   if (cudaGetLastError() != cudaSuccess) return SAF3R_ERR_CUDA;
-  // the join's blocks are set up while the first kernel still runs, and wait for its end on the device
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   const int R = wide ? 16 : 8;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kv.n_heads * ((kv.max_new * p.group + R - 1) / R), kv.n_seqs);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   const auto join = p.e4m3 ? (wide ? decode_join_kernel<true, 2> : decode_join_kernel<true, 1>)
                            : (wide ? decode_join_kernel<false, 2> : decode_join_kernel<false, 1>);
-  if (cudaLaunchKernelEx(&cfg, join, p) != cudaSuccess) return SAF3R_ERR_CUDA;
+  const dim3 items(kv.n_heads * ((kv.max_new * p.group + R - 1) / R), kv.n_seqs);
+  if (launch_behind(join, items, dim3(32 * kJoinWarps), stream, p) != cudaSuccess) return SAF3R_ERR_CUDA;
   ++*n_launch;
   return SAF3R_OK;
 }

@@ -106,6 +106,25 @@ struct KvAttnParams {
 
 #ifdef __CUDACC__
 
+// Two codes (the lower 16 bits) as fp16, exactly; two fp16 values as fp32; two fp32 values rounded to fp16.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two)));
+  return h;
+}
+__device__ __forceinline__ float2 f32x2_of_f16x2(uint32_t h) {
+  float2 v;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(v.x), "=f"(v.y) : "r"(h));
+  return v;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2^e, e in -126 .. 127
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // Sequence b of a batch: its rows, cached length and whether the numbers fit.
 struct SeqInfo {
   int row0, n_new, len;
@@ -215,6 +234,22 @@ __device__ __forceinline__ void rope_sincos(const RopeTable& t, int pair, int po
 }
 
 #endif
+
+// Launches a kernel whose blocks are set up while the one before it in the stream still runs, and which waits for that one's end
+// on the device (griddepcontrol.wait) before it reads what it wrote.
+template <typename Kernel, typename Params>
+cudaError_t launch_behind(Kernel kernel, dim3 grid, dim3 block, cudaStream_t stream, const Params& p) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 bool build_rope_table(const saf3r_rope_cfg* cfg, RopeTable* t);
 cudaError_t launch_rope(const RopeParams& p, bool in_fp32, bool out_fp32, int num_sms, cudaStream_t stream, int* n_launch);

@@ -29,11 +29,7 @@ __device__ __forceinline__ float no_weight() { return __uint_as_float(0x7fffffff
 template <bool kCodes>
 __device__ __forceinline__ float2 pair_of(uint32_t bits) {
   if constexpr (!kCodes) return make_float2(__uint_as_float(bits << 16), __uint_as_float(bits & 0xffff0000u));
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(bits)));
-  float2 v;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(v.x), "=f"(v.y) : "r"(h));
-  return v;
+  return f32x2_of_f16x2(f16x2_of_e4m3(bits));
 }
 
 // Run by one warp: token `row` of the step's tensors, at position pos of sequence b.  Writes columns c0..c1-1.  32 keys at a
