@@ -420,3 +420,70 @@ def test_queries_and_output_of_one_packed_buffer(new):
             hw.saf3r_kv_attn(c.kv, b, win, q, out, ws)
         assert e.value.status == hw.ERR_INVALID
     hw.saf3r_check()
+
+
+@pytest.mark.parametrize("heads,kv_heads,page,new", [(2, 2, 64, [65]), (6, 2, 32, [33, 257, 0, 5]), (5, 1, 128, [100, 0, 7, 52])])
+def test_many_rows_over_8bit_keep_11_bits_of_a_weight(heads, kv_heads, page, new):
+    """fp16 weights: 2^-11 of each, and of n keys at most n 2^-24 of the largest value in all (check_rows' fp16 tolerance)."""
+    hw = _hw()
+    c = Paged(hw, len(new), kv_heads, page, -(-2200 // page), True, seed=page)
+    c.step([700, 31, 0, 450][:len(new)], 1.0, seed=1)
+    for i, mask in enumerate([(1, 0, 0, True), (1, 130, 4, True), (37, 3, 37, True), (37, 2, 300, False), (1, 1, 0, True)]):
+        batch = c.step(new, 0.5 + i % 3, seed=i + 2)
+        g = torch.Generator(device="cuda").manual_seed(i)
+        q = (2 * torch.randn((batch.n_tokens, heads, 64), device="cuda", generator=g)).bfloat16()
+        out, win = torch.empty(q.shape, device="cuda"), hw.make_window(*mask)
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, heads), dtype=torch.uint8, device="cuda")
+        hw.saf3r_kv_attn(c.kv, batch, win, q, out, ws)
+        hw.saf3r_check()
+        t = 0
+        for b, n in enumerate(new):
+            end, idx = int(c.lens[b]), np.arange(0, n, 5)
+            k, v = (O.cached_rows(x, s, c.table[b], end, page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+            for h in range(heads if n else 0):
+                check_rows(_np(out[t:t + n, h])[idx], _np(q[t:t + n, h])[idx], k[:, h // (heads // kv_heads)],
+                           v[:, h // (heads // kv_heads)], end - n + idx, mask, True, False, f"mask {mask}, sequence {b}, head {h}")
+            t += n
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_many_rows_report_numbers_that_do_not_fit(e4m3):
+    hw = _hw()
+    new = 100
+    c = Paged(hw, 1, 2, 16, 20, e4m3, seed=1)
+    good = c.step([new], seed=1)
+    check_step(c, good, [new], 2, (1, 0, 0, True), rows=8)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros((new, 2, 64), device="cuda").bfloat16()
+    win = hw.make_window()
+    for cu, n, m in [([0, new + 1], new + 1, new), ([-1, new], new + 1, new), ([new, 0], new, new), ([0, new], 321, new),
+                     ([0, new], new - 1, new), ([0, new], new, new - 1), ([0, new], -5, new)]:
+        bad = hw.KVBatch(torch.tensor(cu, **i32), torch.tensor([n], **i32), good.page_table, new, m)
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, bad, win, 2), dtype=torch.uint8, device="cuda")
+        hw.saf3r_kv_attn(c.kv, bad, win, q, torch.empty_like(q), ws)
+        with pytest.raises(hw.Saf3rError) as e:
+            hw.saf3r_check()
+        assert e.value.status == hw.ERR_INDEX
+        hw.saf3r_check()
+    check_step(c, good, [new], 2, (1, 0, 0, True), rows=8)
+
+
+def test_an_expired_wait_over_an_8bit_cache_is_reported_and_the_next_call_is_clean():
+    """One softmax warp withholds one arrival: the product warp's wait runs out, nothing hangs."""
+    hw = _hw()
+    c = Paged(hw, 1, 1, 64, 40, True, seed=3)
+    batch = c.step([700], 1.0, seed=1)
+    hw.saf3r_set_wait_budget(20_000_000)
+    try:
+        hw.saf3r_test_withhold_arrive()
+        q = torch.zeros((700, 1, 64), device="cuda").bfloat16()
+        win = hw.make_window()
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(c.kv, batch, win, 1), dtype=torch.uint8, device="cuda")
+        hw.saf3r_kv_attn(c.kv, batch, win, q, torch.empty_like(q), ws)
+        with pytest.raises(hw.Saf3rError) as e:
+            hw.saf3r_check()
+        assert e.value.status == hw.ERR_TIMEOUT
+        hw.saf3r_check()
+        check_step(c, batch, [700], 1, (1, 0, 0, True), rows=12)
+    finally:
+        hw.saf3r_set_wait_budget(0)
