@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
   auto slot = [&](int i) -> const Slot& { return base[2LL * i + (i == i0 ? 1 : 0)]; };
   for (int row = warp / turn; row < rows; row += kJoinWarps / turn) {
     float big = -INFINITY, sum = 0.f, a0 = 0.f, a1 = 0.f;
-    int flags = 0;  // the parts' and, 4: some part's answer is not a number
+    int flags = 0;
     for (int i = i0 + at0; i <= i1; i += 32 * turn) {  // 32 parts at a time
       float w = -INFINITY;
       const int mine = i + lane * turn;
@@ -708,7 +708,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
         const float wk = __shfl_sync(0xffffffffu, w, k);
         const float2 x = reinterpret_cast<const float2*>(slot(i + k * turn).o[row])[lane];
         sum += wk;
-        if (x.x != x.x || x.y != x.y) flags |= 4;
         a0 += wk * x.x;
         a1 += wk * x.y;
       }
@@ -740,9 +739,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const __gr
     a0 *= inv;
     a1 *= inv;
     const bool bad = !(fabsf(a0) <= 3.402823466e+38f && fabsf(a1) <= 3.402823466e+38f);
-    const int i = rg * R + row, tok = p.by_group.div(i), head = hk * p.group + i - tok * p.group;
-    // not finite though no part holds a NaN: the sum left fp32's range
-    if ((flags & 2) || ((flags & 5) != 4 && __any_sync(0xffffffffu, bad))) {
+    const int at_row = rg * R + row, tok = p.by_group.div(at_row), head = hk * p.group + at_row - tok * p.group;
+    bool exact = (flags & 2) != 0;
+    if (!exact && __any_sync(0xffffffffu, bad)) {
+      // a value out of sight is not finite; or no part holds a NaN: the sum left fp32's range
+      bool nan = false;
+      for (int i = i0; i <= i1; ++i) {
+        const float2 x = reinterpret_cast<const float2*>(slot(i).o[row])[lane];
+        nan |= x.x != x.x || x.y != x.y;
+      }
+      exact = (flags & 1) || !__any_sync(0xffffffffu, nan);
+    }
+    if (exact) {
       exact_row<kE4m3>(p, blockIdx.y, s.len, s.row0 + tok, s.len - s.n_new + tok, head, lane, 0, kD);
       continue;
     }
