@@ -487,3 +487,40 @@ def test_an_expired_wait_over_an_8bit_cache_is_reported_and_the_next_call_is_cle
         check_step(c, batch, [700], 1, (1, 0, 0, True), rows=12)
     finally:
         hw.saf3r_set_wait_budget(0)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("new", [1, 90])
+def test_pages_behind_the_first_four_gigabytes(e4m3, new):
+    """The same step over a small cache and over one whose pages in use lie at the far end of pools of 5 GB: the same bits."""
+    hw = _hw()
+    heads, page, per, seqs = 8, 64, 8, 2
+    n_big = 5 * 2 ** 30 // (heads * page * 64 * (1 if e4m3 else 2))
+    g = torch.Generator(device="cuda").manual_seed(new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cfg, win = hw.make_rope((32, 32)), hw.make_window(1, 200, 5)
+    steps = []
+    for n in (300, new):
+        k, v = torch.randn((2, seqs * n, heads, 64), device="cuda", generator=g).bfloat16()
+        steps.append((n, k, v, torch.randint(0, 99, (seqs * n, 2), device="cuda", generator=g).int()))
+    q = torch.randn((seqs * new, 2 * heads, 64), device="cuda", generator=g).bfloat16()
+    outs = []
+    for n_pages in (seqs * per, n_big):
+        kv = hw.PagedKV.empty(n_pages, heads, page, hw.KV_E4M3 if e4m3 else hw.KV_BF16)
+        table = (n_pages - 1 - torch.arange(seqs * per, **i32)).view(seqs, per)
+        done = 0
+        for n, k, v, pos in steps:
+            done += n
+            batch = hw.KVBatch(torch.arange(seqs + 1, **i32) * n, torch.full((seqs,), done, **i32), table, seqs * n, n)
+            hw.saf3r_kv_append(kv, batch, k, v, cfg, pos)
+        out = torch.empty(q.shape, device="cuda")
+        ws = torch.empty(hw.saf3r_kv_attn_workspace_bytes(kv, batch, win, 2 * heads), dtype=torch.uint8, device="cuda")
+        hw.saf3r_kv_attn(kv, batch, win, q, out, ws)
+        hw.saf3r_check()
+        rows = table.long().flatten()
+        outs.append((out, kv.k[rows][:, :, :50].view(torch.uint8).clone(), kv.v[rows][:, :, :50].view(torch.uint8).clone()))
+        del kv
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.isfinite(outs[0][0]).all()
+    used = [i for i in range(seqs * per) if i % per < (300 + new) // page]
+    for a, b in zip(outs[0][1:], outs[1][1:]):
+        assert torch.equal(a[used], b[used])
