@@ -13,7 +13,8 @@
 //          what lies behind a sequence's end need not be finite.  bf16: TMA writes the stage itself.  8-bit: the
 //          codes land beside it, and four more warps (4-7) turn them into fp16 times their page's scale over the
 //          largest of the piece: exact where the scales are within 2^22 of one another; where the values' are not, or
-//          the keys' and it would show, the piece's rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the row's first chunk's largest.
+//          the keys' and it would show, the piece's rows go key by key.  P is fp16 then: 2^-11 of a weight, and 2^-25 of the
+//          row's first chunk's largest.
 //   2-3    issue the products, a warp for each tile.
 //   last 16 softmax: four warpgroups, one for each tile and key half; a thread has one row's 64 keys of a block.
 //          Sixteen warps, four for each scheduler in different steps, hide each other's waits.
@@ -23,13 +24,16 @@
 // Weights are 2^(x - reference), the reference a row's largest logit of its first block: bf16 P and the fp32 sums
 // keep their relative precision at any reference, so no maximum is taken of later blocks.  bf16 weights may grow to 2^64
 // (a row beyond goes key by key); fp16 ones to 2^15, then the reference moves and what was summed so far is scaled.
+// Key by key (stream_exact.cuh) go also rows whose answer is not finite while it may be: next to a masked value that is not, or
+// where the sum of weights times values left fp32's range.  It costs 0.11 us a key and row: one 8-bit view of 1,374 tokens and 16
+// heads over 5,496 keys 83 us, with all rows key by key 5.7 ms.
 //
 // What bounds it: at d = 64 each (query, key) pair is 256 tensor operations and one exponential, and the softmax warps' pipes
 // set the pace: per block of 256 rows and 128 keys 1,792 cycles of the exponential unit (one pair in eight is computed on the
 // FMA pipe: none took 604 us, one in four 571 us, one in eight 556 us) of about 2,350; products take 1,264.  Measured, 16 heads,
-// bf16: 549 us for 10,992 rows and keys = 902 TFLOP/s, 55% of the measured burst rate; long runs meet the power cap and
-// end near 1.5 GHz and 700 TFLOP/s.  8-bit: 237 us for 2 x 1,374 rows over 12,366 keys = 587 TFLOP/s, where the converting
-// warps take the schedulers' slots as well.
+// bf16: 562 us for 10,992 rows and keys = 881 TFLOP/s with the GPU cool, 54% of the measured burst rate; long runs meet the power
+// cap and end near 1.5 GHz and 690 TFLOP/s.  8-bit: 243 us for 2 x 1,374 rows over 12,366 keys = 573 TFLOP/s, where the
+// converting warps take the schedulers' slots as well.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

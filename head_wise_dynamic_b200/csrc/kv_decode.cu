@@ -19,12 +19,12 @@
 //
 // bf16 caches use bf16 products throughout, with the weights in two terms (16 bits): one term alone leaves up to 2^-8 of a row with
 // few weights that count, and one token's 16 rows were 0.0023 to 0.0028 off in all, 0.0017 with two, which is the output's
-// rounding.  It costs nothing at one token (14.3 us), 0.8% at 4 rows per kv head (64 streams of up to 22,000 keys, 4 kv heads:
-// 124 us), 6% at 16 (142 us) and 7% at 64 (289 us).
+// rounding.  It costs nothing at one token (14.4 us), 0.8% at 4 rows per kv head (64 streams of up to 22,000 keys, 4 kv heads:
+// 125 us), 6% at 16 (137 us) and 7% at 64 (276 us).
 // The reference is the largest x of the first step; it moves when a later one exceeds it by 2^15
 // (fp16 P, which ends 2^-24 below it) or 2^24.
 //
-// Measured, 64 8-bit streams of 1 to 22,000 keys, 4 kv heads of 4 query heads: 77 us with the join, 71% of the measured copy
+// Measured, 64 8-bit streams of 1 to 22,000 keys, 4 kv heads of 4 query heads: 79 us with the join, 70% of the measured copy
 // rate.  In its stride a warp's step of 8 KB takes 3,660 cycles with 12 warps an SM, more than that rate;
 // the first step ends 12,000 cycles after the start (lengths, page, scales and codes are four loads that wait for one another).  16-row
 // products straight from global memory, without the transposition, took 216 us.
@@ -766,6 +766,17 @@ int tile_rows(int max_new, int group) { return static_cast<long long>(max_new) *
 
 }  // namespace
 
+// Rows per sequence and kv head that this kernel takes.  It streams the keys once for every 16 rows, the tensor-core kernel once
+// for 256.  Measured, us, here and there:
+//   rows                                        17           32           48           64
+//   8-bit, 4 sequences, 12,000 keys, 16 heads   76 / 79      79 / 79      99 / 79      121 / 79
+//   8-bit, 8 sequences, 4,096 keys, 4 heads     34 / 33      35 / 33      40 / 33      42 / 33
+//   bf16, 4 sequences, 12,000 keys, 16 heads    83 / 66      87 / 66      91 / 66      115 / 66
+//   bf16, 8 sequences, 4,096 keys, 4 heads      31 / 29      32 / 29      34 / 29      36 / 29
+// Up to 16 rows the other one has a tile of 128 rows for them.  From 17 to 64 rows bf16 stays here for its 16 bits of a weight
+// against 8, which callers of short chunks rely on; 8-bit rows stay with it, up to 32 at no cost.  The rule goes by the step's
+// longest sequence: a chunk among single tokens takes all of them there (64 sequences of 1,400 to 23,000 keys, 4 heads of 4, one
+// with 1,374 new tokens: 8-bit 121 us against 41 for the chunk and 35 for the others alone, bf16 87 against 32 and 49).
 bool decode_takes(int max_new, int group) { return static_cast<long long>(max_new) * group <= 64; }
 
 size_t decode_workspace_bytes(const KvView& kv, int group) {

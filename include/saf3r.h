@@ -318,8 +318,8 @@ typedef struct {
  *           attention calls take.
  *   pos:    DEVICE int32 [n_tokens][n_axes], any value
  *   inverse: nonzero turns by minus the angle: the adjoint, so the gradient of x from that of out
- * Angles are exact to 2^-33 turns at every int32 position (64-bit fixed point); the rotation is in
- * fp32 and rounded once.
+ * Angles are worked out in 64-bit fixed point, to 2^-33 turns at every int32 position, and rounded to
+ * fp32 as a part of the nearest quarter turn (2^-28 turns at most); the rotation is in fp32 and rounded once.
  */
 typedef struct {
     int64_t n_tokens;
@@ -365,7 +365,7 @@ typedef struct {
  * follows their contents.  Rows behind the last sequence are not touched.  A sequence whose numbers
  * do not fit (new < 0 or > max_new, rows outside 0 .. n_tokens, kv_lens > max_pages * page, kv_lens < new) or
  * that needs a page outside the cache records SAF3R_ERR_INDEX: nothing is read or written outside the
- * buffers, that sequence's results are unspecified.
+ * buffers, that sequence's results are unspecified (where cu_tokens runs back, those of sequences behind it too).
  */
 typedef struct {
     int32_t n_seqs;     /* 0..65535 */
@@ -388,13 +388,14 @@ typedef struct {
 
 /*
  * Append the new tokens' keys and values to the cache.
- *   rope: keys are rotated on the way (fp32, rounded once to the cache's type); NULL: as they are.
+ *   rope: keys are rotated on the way (fp32, rounded once to the cache's type; for SAF3R_KV_E4M3 scales and codes are
+ *     those of the exact rotation, to its angle's 2^-33 turns); NULL: as they are.
  *   SAF3R_KV_E4M3: of each (page, head), keys and values apart, the scale becomes
  *     2^ceil(log2(m / 448)), m the largest finite magnitude among the new rows, but at least 2^-100, and not
  *     less than the scale of the page's older rows when it has any; where that grew, the older rows' codes are
  *     rounded again to the new scale (exact but for codes that become subnormal).  Codes are rounded to nearest,
  *     ties to even; infinities and NaN become NaN.
- * A page may take new rows of one sequence only; pages shared by sequences must be full.
+ * A page may take new rows of one sequence only, and once in its row of page_table; pages shared by sequences must be full.
  */
 saf3r_status saf3r_kv_append(const saf3r_kv_cache* cache, const saf3r_kv_batch* batch,
                              const saf3r_rope_cfg* rope, const saf3r_kv_rows* rows, void* stream);
@@ -431,11 +432,26 @@ size_t saf3r_kv_attn_workspace_bytes(const saf3r_kv_cache* cache, const saf3r_kv
  * Attention of each sequence's new tokens to its cached tokens, themselves among them (append first):
  * softmax(q . k / sqrt(64)) over the tokens that `window` lets them see.  Pages without a visible token are not
  * read: the caller may have given them to others.  Up to 64 rows per sequence and kv head (max_new * heads per kv head)
- * take a kernel that splits the keys over the GPU; more the tensor-core kernel.  Weights are rounded once, to bf16 (16 bits in
- * the kernel for up to 64 rows) or, over 8-bit caches, to fp16 (where those below 2^-14 of a row's first logits' largest weight
- * lose bits, 2^-25 of it at most); sums are in fp32.  What a masked token holds never reaches a row: next to one whose values
- * are not finite (up to 64 rows over bf16 caches: also at one in sight), and where the value scales of a row's pages are more
- * than 2^22 apart, rows are computed key by key, at a small fraction of the speed.
+ * take a kernel that splits the keys over the GPU; more the tensor-core kernel.  The longest sequence of the step decides for
+ * all of them: one long chunk among single tokens costs these a tile of 128 rows each.
+ * Weights are rounded once: over bf16 caches to 16 bits for up to 64 rows and to bf16's 8 bits from 65 on (the error of a row
+ * grows from the output's rounding, 0.0017 of it, to 0.0024); over 8-bit caches to fp16 (those below 2^-14 of a row's first
+ * logits' largest weight lose bits, 2^-25 of it at most).  Over 8-bit caches a row's queries are fp16 relative to its largest
+ * (what is below 2^-14 of that loses bits, 2^-25 of it at most).  The tensor-core kernel computes one exponential in eight by a
+ * cubic (8.6e-5 of the weight).  Sums are in fp32.
+ * What a masked token holds never reaches a row.  A row is computed key by key, in fp32 at 0.11 us a key (70 times as long as the
+ * other rows of a view),
+ *   - next to a masked token whose values are not finite, and where a value in sight is infinite (up to 64 rows over bf16
+ *     caches: or NaN);
+ *   - where its values are so large that sums of them leave fp32's range (from about 1e34 on);
+ *   - over 8-bit caches where the value scales of its pages are far apart: more than 2^64 for up to 64 rows, else 2^22 (pages of
+ *     zeros, of scale 2^-100, do not count); and, from 65 rows on, where the key scales are more than 2^22 apart and the row's
+ *     largest query times the largest key exceeds about 2^15;
+ *   - from 65 rows on over bf16 caches where later logits exceed the largest of the first 128 keys of the row (or of one of the
+ *     parts that its keys are cut into) by 44 (a weight of 2^64).
+ * A warp may have 32 such rows while others wait for it: over more than half a million keys raise saf3r_set_wait_budget, or
+ * the call may end with SAF3R_ERR_TIMEOUT.
+ * A row whose logits are all minus infinity, or of which one is plus infinity or NaN, is NaN.
  * workspace: DEVICE, 16-byte aligned, saf3r_kv_attn_workspace_bytes bytes, used by one call at a time
  * (also when calls are captured: graphs that share it must not overlap); it needs no start value.
  */
@@ -447,8 +463,8 @@ size_t saf3r_window_attn_workspace_bytes(const saf3r_layout* layout, const saf3r
 
 /*
  * Attention over views held at once, q, k, v and out as saf3r_dense_attn, each token seeing what `window`
- * says (view_tokens is usually the layout's V, but need not be).  out overlaps none of the others.  Workspace as
- * saf3r_kv_attn.
+ * says (view_tokens is usually the layout's V, but need not be).  out overlaps none of the others.  Workspace, precision and
+ * rows computed key by key as saf3r_kv_attn with more than 64 rows over a bf16 cache.
  */
 saf3r_status saf3r_window_attn(const saf3r_layout* layout, const saf3r_window* window, const void* q, const void* k,
                                const void* v, void* out, int out_is_fp32, void* workspace, void* stream);
