@@ -12,7 +12,7 @@
 //
 // Measured: 16 views of bf16 (1,374 tokens, 16 heads, pages of 16) 39 us, 70% of the measured copy rate: 4 loads that wait
 // for one another before a block's first row is stored, three waves of blocks.  Fewer heads a block cost more
-// (8: 44 us, 4: 60 us), as does putting the rows together in shared memory first (45 us).  One 8-bit view 15 us: instructions (37%
+// (8: 44 us, 4: 60 us), as does putting the rows together in shared memory first (45 us).  One 8-bit view 16 us: instructions (37%
 // of the issue slots, 6 us of pure issue: values turned twice, codes made four times over to find those next to a border) and
 // the same chain.  64 single tokens 4.3 us of GPU time (a call takes 7.6 us of the host): latency.
 #include "rope.cuh"

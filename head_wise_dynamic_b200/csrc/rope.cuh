@@ -53,13 +53,26 @@ __device__ __forceinline__ void spread(const Segment<T, N>& u, const Segment<T, 
   }
 }
 
+// A value as it is, or from 64 bits to fp32 to odd: cut off, with the last bit set where that was not exact.  It lies on the
+// value's side of every border between two codes of fewer bits; rounded to nearest it could fall on the border itself and
+// from there, a tie, to the wrong side.
+template <typename V, typename T>
+__device__ __forceinline__ V narrow(T x) {
+  if constexpr (sizeof(T) == sizeof(V)) {
+    return x;
+  } else {
+    const float f = __double2float_rz(x);
+    return static_cast<double>(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+  }
+}
+
 // Turns the segments' N pairs: (a[i], b[i]), or neighbours inside each segment.  T: what the products are held in, V: the
 // values.
 template <typename V, typename T>
 __device__ __forceinline__ void turn_pair(V& a, V& b, T s, T c) {
   const T x = a, y = b;
-  a = static_cast<V>(x * c - y * s);
-  b = static_cast<V>(x * s + y * c);
+  a = narrow<V>(x * c - y * s);
+  b = narrow<V>(x * s + y * c);
 }
 template <typename V, typename T, int N>
 __device__ __forceinline__ void turn(V (&a)[N], V (&b)[N], const T (&s)[N], const T (&c)[N], bool interleaved) {

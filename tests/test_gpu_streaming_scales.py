@@ -62,3 +62,41 @@ def test_scales_next_to_a_border(dims, pairing, many):
             s = O.scale_of(np.abs(x).max())
             assert scale[i, h] == s, (rows[i], h, scale[i, h], s)
             assert np.array_equal(codes[i, h, :per], O.round_e4m3(x / s))
+
+
+@pytest.mark.parametrize("pairing", [0, 1, 2])
+@pytest.mark.parametrize("many", [False, True])
+def test_codes_next_to_a_tie(pairing, many):
+    """Values 2^-27 from the middle between two codes on either side: fp32 would put them on it."""
+    hw = _hw()
+    base, page, dims = 1e12, 16, (40,)
+    rows = []
+    for first, second, axis, freq in O.rope_pairs(dims, base, pairing):
+        if not 2e-11 < freq < 1e-9:
+            continue
+        for a, middle in ((58.25, 58.0), (62.25, 62.0), (54.25, 54.0), (50.25, 50.0)):
+            p = _crossing(a, 32.0, freq, middle)
+            off = max(1, int(middle * 2.0 ** -27 / (32.0 * freq)))
+            rows += [(first, second, a, p + d) for d in (-off, off)]
+    T, H = len(rows), 2
+    assert T >= 8
+    per = 3 if many else 1
+    k = torch.zeros((T * per, H, 64))
+    pos = torch.zeros((T * per, 1), dtype=torch.int32)
+    for i, (first, second, a, p) in enumerate(rows):
+        at = per * i + per // 2
+        k[at, :, first], k[at, :, second], k[at, :, 63] = a, 32.0, 448.0  # dims from 40 on are not rotated: the scale is 1
+        k[at, 1] *= -1.0
+        pos[at, 0] = p
+    k = k.bfloat16()
+    want = O.round_e4m3(O.rope(_np(k), pos.numpy(), dims, base, pairing))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = hw.PagedKV.empty(T, H, page)
+    batch = hw.KVBatch(torch.arange(T + 1, **i32) * per, torch.full((T,), per, **i32), torch.arange(T, **i32).view(T, 1), T * per, per)
+    kd = k.cuda()
+    hw.saf3r_kv_append(cache, batch, kd, torch.zeros_like(kd), hw.make_rope(dims, base, pairing), pos.cuda())
+    hw.saf3r_check()
+    assert (cache.k_scale == 1.0).all()
+    codes = _np(cache.k.float())
+    for i in range(T):
+        assert np.array_equal(codes[i, :, :per], want[per * i:per * (i + 1)].transpose(1, 0, 2)), rows[i]
